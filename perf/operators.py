@@ -74,12 +74,12 @@ def draw(rng):
         else:
             e = rng.choice([2, 4, 8, 16, 32, 64])
             c = {"op": op, "t": _log(rng, 1, 64), "e": e, "top": rng.randint(1, min(e, 8)),
-                 "d": _log(rng, 256, 4096, 32), "f": _log(rng, 256, 8192, 32), "bits": rng.choice([2, 3, 4]),
+                 "d": _log(rng, 256, 4096, 32), "f": _log(rng, 256, 12288, 32), "bits": rng.choice([2, 3, 4]),
                  "x": rng.choice(list(DT)), "y": rng.choice(list(DT)), "act": rng.choice(["silu", "relu"]),
                  "renorm": rng.random() < 0.5}
             groups = [g for g in (32, 64, 128) if c["d"] % g == 0 and c["f"] % g == 0]
             c["group"] = rng.choice([0] + groups)
-            fits = c["e"] * c["d"] * c["f"] <= 2 * 10 ** 8
+            fits = c["e"] * c["d"] * c["f"] <= 36 * 10 ** 7
         if fits:
             return c
 
