@@ -274,6 +274,58 @@ GPTQ_API gptq_status gptq_dequantize(const int32_t* packed, const float* scales,
                                      void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * 8-bit floating-point operands (e4m3: one sign bit, four exponent bits, three mantissa bits, largest
+ * value 448, no infinities) with one fp32 scale per block of 128 columns, for answering many rows
+ * (prompts) on the fp8 tensor cores: the step after the path at the other end of the batch range from
+ * gptq_dequant_matmul (FDE breakdown, section 01, last paragraph).
+ *
+ * gptq_fp8_quantize: Q[r, j] = e4m3(X[r, j] / s), s the scale of the block that holds (r, j).
+ *   Blocks span 128 columns and block_rows rows: 1 (activations) or 128 (weights); blocks at the right
+ *   and lower edges are cut off.  With a = max |x| over the finite values of the block, s = 2^e for the
+ *   smallest integer e >= -126 with a <= 448 * 2^e, and s = 1 when a = 0.  A division by a power of
+ *   two is exact, so rounding to e4m3 (to nearest, ties to even) is the only rounding.  NaN and
+ *   infinite values become the NaN code and leave the scale alone.
+ *   X          [m, k] row-major, BF16 / FP16 / FP32, 16-byte aligned; k % 16 == 0; m may be 0.
+ *   Q          [m, k] e4m3 output, 16-byte aligned; must not overlap X.
+ *   scales     [ceil(m / block_rows), ceil(k / 128)] fp32 output.
+ *
+ * gptq_fp8_from_packed: a quantized layer as e4m3 operands without any rounding: Q[r, j] = q[r, j] -
+ * zero[r, g(j)], an integer of magnitude <= 15 (e4m3 holds integers up to 16), and the grid's scale as
+ * the scale of the row's block of 128 columns: What[r, j] = scales_out[r, j / 128] * Q[r, j].
+ *   packed     [m, k*bits/32] int32 (gptq_pack), 4-byte aligned; scales / zeros [m, n_groups] as written by
+ *              gptq_quantize_layer (zeros in [0, 2^bits - 1]; others are rounded to the nearest e4m3 value,
+ *              at most 448).  k % 32 == 0, bits in {2, 3, 4}.
+ *   group_size 0 (one grid per row) or a multiple of 128 that divides k.  A group of 32 or 64 puts more
+ *              than one scale into a block of 128: GPTQ_ERR_UNSUPPORTED.
+ *   Q          [m, k] e4m3 output, 16-byte aligned.
+ *   scales_out [m, ceil(k / 128)] fp32 output.
+ *
+ * gptq_fp8_matmul: Y[i, j] = sum over blocks b of 128 columns of
+ *     a_scales[i, b] * b_scales[j / b_block_rows, b] * (sum over t in block b of A[i, t] * B[j, t]).
+ *   A          [m, k] e4m3 (activations), B [n, k] e4m3 (weights), 16-byte aligned; k % 16 == 0, 16 <= k.
+ *              m may be 0 (nothing is enqueued); m, n, k <= 2^20.
+ *   a_scales   [m, ceil(k / 128)] fp32;  b_scales [ceil(n / b_block_rows), ceil(k / 128)] fp32, any
+ *              values; b_block_rows 1 (gptq_fp8_from_packed) or 128 (gptq_fp8_quantize).
+ *   Y          [m, n] row-major, y_dtype BF16 / FP16 / FP32 (rounded once from the fp32 sum).
+ *   dev_status int32[2], zeroed by the caller once: GPTQ_ERR_TIMEOUT is recorded if a bounded wait gave up.
+ *              Not cleared by the call, so one word can watch a chain of calls.
+ *   workspace  >= gptq_fp8_matmul_workspace_size(m, n, k) bytes, 256-byte aligned (may be NULL when
+ *              that is 0).  Calls that may overlap on the GPU, captured graphs among them, each need
+ *              their own.
+ *   Block products run on the tensor cores with fp32 accumulation, the scaled sum over blocks in fp32
+ *   registers; split sums are added in a fixed order, so results are deterministic.
+ * ------------------------------------------------------------------------------------------ */
+GPTQ_API gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int32_t block_rows,
+                                       void* Q, float* scales, void* stream);
+GPTQ_API gptq_status gptq_fp8_from_packed(const int32_t* packed, const float* scales, const int32_t* zeros, int64_t m,
+                                          int64_t k, int32_t bits, int32_t group_size, void* Q, float* scales_out,
+                                          void* stream);
+GPTQ_API gptq_status gptq_fp8_matmul(const void* A, const float* a_scales, const void* B, const float* b_scales,
+                                     int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* Y, int32_t y_dtype,
+                                     int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+GPTQ_API size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* ------------------------------------------------------------------------------------------
  * Status helpers.
  * gptq_read_status: synchronizes `stream`, copies the device status word to the host, returns the
  * code it holds (GPTQ_OK if clear) and stores its detail (e.g. the failing pivot) in *detail when

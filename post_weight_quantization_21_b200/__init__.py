@@ -11,6 +11,11 @@ the first call raises.
     packed int32 words                gptq_pack
     act-order (desc_act)              gptq_act_order + gptq_quantize_layer_act_order
 
+and the calls that answer with the result:
+
+    Y = X What^T, a few rows          gptq_dequant_matmul   (packed codes)
+    Y = X What^T, many rows           gptq_fp8_from_packed once, then gptq_fp8_quantize + gptq_fp8_matmul
+
 ``LayerSolver`` strings the four calls together over preallocated buffers.
 """
 from __future__ import annotations
@@ -26,6 +31,7 @@ __all__ = [
     "gptq_read_status", "gptq_status_string", "gptq_kernel_launches", "gptq_tensor_core_phases", "LayerSolver", "LIB_PATH", "ABI_FUNCTIONS",
     "gptq_act_order", "gptq_quantize_layer_act_order", "gptq_quantize_act_order_workspace_size", "act_order_group_index",
     "gptq_dequant_matmul", "gptq_dequant_matmul_workspace_size", "gptq_dequantize",
+    "gptq_fp8_quantize", "gptq_fp8_from_packed", "gptq_fp8_matmul", "gptq_fp8_matmul_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
@@ -65,6 +71,10 @@ ABI_FUNCTIONS = {
                                    _vp]),
     "gptq_dequant_matmul_workspace_size": (_sz, [_i64, _i64, _i64]),
     "gptq_dequantize": (_i32, [_vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _i32, _vp]),
+    "gptq_fp8_quantize": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "gptq_fp8_from_packed": (_i32, [_vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "gptq_fp8_matmul": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "gptq_fp8_matmul_workspace_size": (_sz, [_i64, _i64, _i64]),
     "gptq_read_status": (_i32, [_vp, _vp, ctypes.POINTER(_i64)]),
     "gptq_status_string": (ctypes.c_char_p, [_i32]),
     "gptq_abi_version": (_i32, []),
@@ -262,6 +272,83 @@ def gptq_dequantize(packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Ten
     m, d = W_hat.shape
     _check(lib().gptq_dequantize(_ptr(packed), _ptr(scales), _ptr(zeros), m, d, bits, group_size, _ptr(W_hat),
                                  _DTYPES[W_hat.dtype], _stream(stream)), "gptq_dequantize")
+
+
+# ------------------------------------------------------------------------------------------ fp8 operands
+def _shaped(t: torch.Tensor, name: str, shape: tuple, dtype, dev):
+    """A contiguous tensor of this shape and type (one type or a mapping of types) on ``dev``."""
+    if t.shape != shape or not (t.dtype in dtype if isinstance(dtype, dict) else t.dtype == dtype):
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} "
+                         f"{' / '.join(map(str, dtype)) if isinstance(dtype, dict) else dtype}")
+    if t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+
+
+def _on(dev: torch.device, stream, call):
+    """``call(stream)`` with ``dev`` current: the library launches on the current device."""
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def gptq_fp8_quantize(X: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, stream=None):
+    """Q [m, k] (torch.float8_e4m3fn) and scales (fp32, powers of two) with X ~ scale * Q: one scale per 128
+    columns and ``block_rows`` rows (1 for activations, 128 for weights)."""
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows {block_rows}: 1 or 128")
+    m, k = X.shape
+    dev = X.device
+    _shaped(X, "X", (m, k), _DTYPES, dev)
+    _shaped(Q, "Q", (m, k), torch.float8_e4m3fn, dev)
+    _shaped(scales, "scales", (-(-m // block_rows), -(-k // 128)), torch.float32, dev)
+    st = _on(dev, stream, lambda s: lib().gptq_fp8_quantize(_ptr(X), _DTYPES[X.dtype], m, k, block_rows, _ptr(Q),
+                                                             _ptr(scales), s))
+    _check(st, "gptq_fp8_quantize")
+
+
+def gptq_fp8_from_packed(packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, bits: int, group_size: int,
+                         Q: torch.Tensor, q_scales: torch.Tensor, stream=None):
+    """A quantized layer as e4m3 operands, without rounding: Q [m, k] = q - zero and q_scales [m, ceil(k / 128)] the
+    grids' scales (group_size 0 or a multiple of 128)."""
+    m, k = Q.shape
+    dev = Q.device
+    ng = k // group_size if group_size > 0 else 1
+    _shaped(Q, "Q", (m, k), torch.float8_e4m3fn, dev)
+    _shaped(packed, "packed", (m, k * bits // 32), torch.int32, dev)
+    _shaped(scales, "scales", (m, ng), torch.float32, dev)
+    _shaped(zeros, "zeros", (m, ng), torch.int32, dev)
+    _shaped(q_scales, "q_scales", (m, -(-k // 128)), torch.float32, dev)
+    st = _on(dev, stream, lambda s: lib().gptq_fp8_from_packed(_ptr(packed), _ptr(scales), _ptr(zeros), m, k, bits,
+                                                                group_size, _ptr(Q), _ptr(q_scales), s))
+    _check(st, "gptq_fp8_from_packed")
+
+
+def gptq_fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    return lib().gptq_fp8_matmul_workspace_size(m, n, k)
+
+
+def gptq_fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor,
+                    b_block_rows: int, Y: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """Y [m, n] (bf16 / fp16 / fp32) = A [m, k] @ B [n, k]^T for e4m3 operands with a scale per 128 columns and row of
+    A, and per 128 columns and ``b_block_rows`` (1 or 128) rows of B."""
+    if b_block_rows not in (1, 128):
+        raise ValueError(f"b_block_rows {b_block_rows}: 1 or 128")
+    m, k = A.shape
+    n = B.shape[0]
+    kb, dev = -(-k // 128), A.device
+    _shaped(A, "A", (m, k), torch.float8_e4m3fn, dev)
+    _shaped(B, "B", (n, k), torch.float8_e4m3fn, dev)
+    _shaped(a_scales, "a_scales", (m, kb), torch.float32, dev)
+    _shaped(b_scales, "b_scales", (-(-n // b_block_rows), kb), torch.float32, dev)
+    _shaped(Y, "Y", (m, n), _DTYPES, dev)
+    _shaped(status, "status", (2,), torch.int32, dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    st = _on(dev, stream, lambda s: lib().gptq_fp8_matmul(
+        _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), b_block_rows, m, n, k, _ptr(Y), _DTYPES[Y.dtype],
+        _ptr(status), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+    _check(st, "gptq_fp8_matmul")
 
 
 def gptq_tensor_core_phases(m: int, d: int, n_tokens: int, x_dtype, bits: int, group_size: int = 0,

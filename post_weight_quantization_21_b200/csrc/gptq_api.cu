@@ -217,6 +217,53 @@ gptq_status gptq_dequantize(const int32_t* packed, const float* scales, const in
                                  static_cast<cudaStream_t>(stream));
 }
 
+gptq_status gptq_fp8_quantize(const void* X, int32_t x_dtype, int64_t m, int64_t k, int32_t block_rows, void* Q,
+                              float* scales, void* stream) {
+  if (m < 0 || k <= 0 || k % 16 || k > kMaxDim || m > kMaxDim * 64 || !valid_dtype(x_dtype)) return GPTQ_ERR_ARG;
+  if (block_rows != 1 && block_rows != 128) return GPTQ_ERR_ARG;
+  if (m == 0) return GPTQ_OK;
+  if (!X || !Q || !scales || X == Q) return GPTQ_ERR_ARG;
+  if (!aligned(X, 16) || !aligned(Q, 16) || !aligned(scales, 4)) return GPTQ_ERR_ARG;
+  return gptq::fp8_quantize_launch(X, x_dtype, m, k, block_rows, Q, scales, static_cast<cudaStream_t>(stream));
+}
+
+gptq_status gptq_fp8_from_packed(const int32_t* packed, const float* scales, const int32_t* zeros, int64_t m,
+                                 int64_t k, int32_t bits, int32_t group_size, void* Q, float* scales_out,
+                                 void* stream) {
+  if (m < 0 || k <= 0 || k % 32 || k > kMaxDim || m > kMaxDim * 64 || bits < 2 || bits > 4) return GPTQ_ERR_ARG;
+  if (group_size < 0 || (group_size && (group_size % 32 || k % group_size))) return GPTQ_ERR_ARG;
+  if (group_size % 128) return GPTQ_ERR_UNSUPPORTED;
+  if (m == 0) return GPTQ_OK;
+  if (!packed || !scales || !zeros || !Q || !scales_out) return GPTQ_ERR_ARG;
+  if (!aligned(packed, 4) || !aligned(scales, 4) || !aligned(zeros, 4) || !aligned(Q, 16) || !aligned(scales_out, 4))
+    return GPTQ_ERR_ARG;
+  if ((const void*)scales == (const void*)scales_out) return GPTQ_ERR_ARG;
+  return gptq::fp8_from_packed_launch(packed, scales, zeros, m, k, bits, group_size, Q, scales_out,
+                                      static_cast<cudaStream_t>(stream));
+}
+
+size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim || k % 16) return 0;
+  return gptq::fp8_matmul_workspace(m, n, k);
+}
+
+gptq_status gptq_fp8_matmul(const void* A, const float* a_scales, const void* B, const float* b_scales,
+                            int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* Y, int32_t y_dtype,
+                            int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream) {
+  if (m < 0 || n <= 0 || k <= 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim || k % 16 || !valid_dtype(y_dtype))
+    return GPTQ_ERR_ARG;
+  if (b_block_rows != 1 && b_block_rows != 128) return GPTQ_ERR_ARG;
+  if (m == 0) return GPTQ_OK;
+  if (!A || !a_scales || !B || !b_scales || !Y || !dev_status) return GPTQ_ERR_ARG;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
+      !aligned(Y, dtype_size(y_dtype)) || !aligned(dev_status, 4))
+    return GPTQ_ERR_ARG;
+  const size_t need = gptq::fp8_matmul_workspace(m, n, k);
+  if (need && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))) return GPTQ_ERR_WORKSPACE;
+  return gptq::fp8_matmul_launch(A, a_scales, B, b_scales, b_block_rows, m, n, k, Y, y_dtype, dev_status, workspace,
+                                 static_cast<cudaStream_t>(stream));
+}
+
 gptq_status gptq_read_status(const int32_t* dev_status, void* stream, int64_t* detail) {
   if (dev_status == nullptr) return GPTQ_ERR_ARG;
   int32_t h[2] = {0, 0};

@@ -116,6 +116,17 @@ gptq_status dequant_matmul_launch(const int32_t* packed, const float* scales, co
 gptq_status dequantize_launch(const int32_t* packed, const float* scales, const int32_t* zeros, int64_t m, int64_t d,
                               int32_t bits, int32_t group_size, void* out, int32_t out_dtype, cudaStream_t stream);
 
+// 8-bit floating-point operands and their product (fp8_operands.cu, fp8_matmul.cu)
+gptq_status fp8_quantize_launch(const void* X, int32_t x_dtype, int64_t m, int64_t k, int32_t block_rows, void* Q,
+                                float* scales, cudaStream_t stream);
+gptq_status fp8_from_packed_launch(const int32_t* packed, const float* scales, const int32_t* zeros, int64_t m,
+                                   int64_t k, int32_t bits, int32_t group_size, void* Q, float* scales_out,
+                                   cudaStream_t stream);
+size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k);
+gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* B, const float* b_scales,
+                              int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* Y, int32_t y_dtype,
+                              int32_t* status, void* workspace, cudaStream_t stream);
+
 // A7
 gptq_status pack_launch(const uint8_t* codes, int64_t m, int64_t d, int32_t bits, int32_t* packed,
                         cudaStream_t stream);
