@@ -3,18 +3,22 @@
 //
 // The scales change every 128 columns, so the tensor cores can only carry the sum inside one block: each
 // P_b is a fresh accumulator in TMEM, and the scaled sum over b runs in fp32 registers of the epilogue
-// warps while the MMAs of the next blocks proceed into the other accumulators.  Weights (B) take the
-// M side of the MMA, tokens (A) the N side: a TMEM lane is a weight row, so its scale is one register per
-// thread and block, the tokens' scales come from shared memory as a vector common to all lanes
-// (two fp32x2 operations per two products), and a handful of tokens costs a tile 16 columns wide, not 128.
+// warps while the MMAs of the next blocks proceed into the other accumulators.  The epilogue reads TMEM
+// in the 16x256b shape: a thread holds four token rows and column pairs, so a block costs it four row
+// scales and, where every weight row has its own scale, one 8-byte shared-memory load per 8 columns of
+// the warp.  (In the 32x32b shape, a row per thread, the column scales are the same for all lanes, and
+// those broadcast loads alone took over 1000 shared-memory cycles per 128 x 256 block: 683 us instead of
+// the time below.)  Two fp32x2 operations per two products, or one where 128 weight rows share a scale,
+// which is then multiplied into the row scales.
 //
-// One CTA per SM, persistent.  A unit is a tile of 128 weight rows x NT tokens and a range of blocks:
+// One CTA per SM, persistent.  A unit is a tile of 128 tokens x NT weight rows and a range of blocks:
 //   warp 0      TMA producer: ring of stages, one block (128 bytes of every row) each
 //   warp 1      tcgen05.mma kind::f8f6f4 issuer (one thread) and TMEM owner: four K = 32 steps per block
-//   warps 2-9   epilogue: 32 rows x NT / 2 tokens per warp
+//   warps 4-11  epilogue: 32 tokens x NT / 2 weight rows per warp
 // Every mbarrier wait is bounded; on a timeout the kernel records GPTQ_ERR_TIMEOUT, the other roles
 // leave, copies and MMAs in flight land, TMEM is freed.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "tc_common.cuh"
@@ -24,31 +28,34 @@ namespace {
 
 using namespace tc;
 
-constexpr int BM = 128;           // weight rows per tile
+constexpr int BM = 128;           // tokens per tile
 constexpr int BK = 128;           // columns per block (and per stage): 128 bytes, one swizzle row
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + EPI_WARPS * 32;
 constexpr int SG = 8;             // blocks whose token scales are staged at a time
 constexpr int kPlanSMs = 148;
-constexpr int kGroupTiles = 16;   // weight tiles walked together (see unit_coords)
+constexpr int kGroupTiles = 16;   // token tiles walked together (see unit_coords)
 constexpr int kSmemBudget = 200 * 1024;
 
 template <int NT>
 struct Cfg {
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kEpiThreads = kEpiWarps * 32;
+  static constexpr int kThreads = 128 + kEpiThreads;
   static constexpr int kStageBytes = (BM + NT) * BK;
   static constexpr int kStages = kSmemBudget / kStageBytes > 10 ? 10 : kSmemBudget / kStageBytes;
-  static constexpr int kAccs = NT >= 256 ? 2 : 4;  // accumulators in TMEM
+  static constexpr int kAccs = 4;  // accumulators in TMEM
   static constexpr int kTmemCols = NT * kAccs < 32 ? 32 : NT * kAccs;
-  static constexpr int kCols = NT / 2;  // tokens per epilogue thread
-  static constexpr int kScaleBytes = 2 * SG * NT * 4;
+  static constexpr int kCols = NT * 4 / kEpiWarps;  // weight rows per epilogue warp
+  static constexpr int kScaleRow = 2 * BM > BM + NT ? 2 * BM : BM + NT;  // staged scales per block
+  static constexpr int kScaleBytes = 2 * SG * kScaleRow * 4;
   static constexpr int kSmem = kStages * kStageBytes + kScaleBytes + 1024 + 512;
 };
 
 struct Args {
   int m, n, kb;                    // tokens, weight rows, blocks
-  int tiles_w, tiles_t, units;     // weight tiles, token tiles, work units
+  int tiles_t, tiles_w, units;     // token tiles, weight tiles, work units
   int kb_per_split;
-  int b_shift;                     // weight row -> row of b_scales: 0 or 7
+  bool vec_scales, vec_y;          // 16-byte accesses to the scales' and Y's rows are aligned
+  int token_bytes;                 // bytes of a stage's token box (fewer than 128 rows when m is small)
   uint32_t idesc;
   const float* a_scales;
   const float* b_scales;
@@ -67,23 +74,15 @@ __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_
       : "memory");
 }
 
-// 8 or 16 consecutive TMEM columns of this warp's 32 lanes; the values are there after tmem_wait()
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]);
+// 16 TMEM lanes x 8 J columns: r[4 j + {0, 1}] are columns 8 j + 2 (lane % 4) + {0, 1} of row lane / 4,
+// r[4 j + {2, 3}] the same columns of row lane / 4 + 8; there after tmem_wait()
+template <int J>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r);
 template <>
-__device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+__device__ __forceinline__ void tmem_ld<2>(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
-}
-template <>
-__device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
@@ -108,17 +107,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
-// unit -> (weight tile, token tile, split).  Weight tiles are walked in groups of kGroupTiles, all token
+// unit -> (token tile, weight tile, split).  Token tiles are walked in groups of kGroupTiles, all weight
 // tiles for each group, so that the tiles in flight share few rows of either operand in L2.
-__device__ __forceinline__ void unit_coords(int u, const Args& a, int& tw, int& tt, int& s) {
+__device__ __forceinline__ void unit_coords(int u, const Args& a, int& tt, int& tw, int& s) {
   const int tiles = a.tiles_w * a.tiles_t;
   s = u / tiles;
   const int t = u % tiles;
-  const int g = t / (kGroupTiles * a.tiles_t);
-  const int w = min(kGroupTiles, a.tiles_w - g * kGroupTiles);
-  const int r = t - g * kGroupTiles * a.tiles_t;
-  tw = g * kGroupTiles + r % w;
-  tt = r / w;
+  const int g = t / (kGroupTiles * a.tiles_w);
+  const int w = min(kGroupTiles, a.tiles_t - g * kGroupTiles);
+  const int r = t - g * kGroupTiles * a.tiles_w;
+  tt = g * kGroupTiles + r % w;
+  tw = r / w;
 }
 
 template <typename T>
@@ -130,14 +129,59 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-template <int NT, typename TY>
-__global__ void __launch_bounds__(THREADS, 1)
-    fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t,
+// two neighbouring results of a row; `pair`: both exist and y is aligned for both
+template <typename T>
+__device__ __forceinline__ void store_pair(T* y, float v0, float v1, int left, bool pair) {
+  if (pair) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float2*>(y) = make_float2(v0, v1);
+    } else {
+      T h[2] = {from_f32<T>(v0), from_f32<T>(v1)};
+      *reinterpret_cast<uint32_t*>(y) = *reinterpret_cast<uint32_t*>(h);
+    }
+  } else {
+    if (left > 0) y[0] = from_f32<T>(v0);
+    if (left > 1) y[1] = from_f32<T>(v1);
+  }
+}
+
+// NC consecutive results of one row, `left` of which exist
+template <int NC, typename T>
+__device__ __forceinline__ void store_row(const uint64_t (&acc)[NC / 2], T* y, int left) {
+#pragma unroll
+  for (int c = 0; c < NC; c += 2) {
+    float v0, v1;
+    unpack2(acc[c / 2], v0, v1);
+    if (c < left) y[c] = from_f32<T>(v0);
+    if (c + 1 < left) y[c + 1] = from_f32<T>(v1);
+  }
+}
+
+// scales of blocks g0 .. g0 + N - 1 of one row (zero past the last block b1); vec: rows start on 16 bytes and
+// g0 is a multiple of 4.  One row's scales are kb floats away from the next row's, so every lane reads a
+// line of its own: two 16-byte loads take a quarter of eight 4-byte loads' time in the load unit.
+template <int N>
+__device__ __forceinline__ void fetch_scales(const float* p, int g0, int b1, bool vec, float (&v)[N]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 f = g0 + i < b1 ? __ldg(reinterpret_cast<const float4*>(p + g0 + i)) : make_float4(0, 0, 0, 0);
+      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = g0 + i < b1 ? __ldg(p + g0 + i) : 0.0f;
+  }
+}
+
+template <int NT, bool BLOCK, typename TY>
+__global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
+    fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
                       const Args a) {
   using C = Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* token_scales = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);  // [2][SG][NT]
+  float* token_scales = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);  // [2][SG][kScaleRow]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes + C::kScaleBytes);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
@@ -154,7 +198,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < C::kAccs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], EPI_WARPS);
+      mbar_init(&acc_empty[b], C::kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -172,8 +216,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t stage = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-        int tw, tt, s;
-        unit_coords(u, a, tw, tt, s);
+        int tt, tw, s;
+        unit_coords(u, a, tt, tw, s);
         const int b0 = s * a.kb_per_split, b1 = min(a.kb, b0 + a.kb_per_split);
         for (int b = b0; b < b1; ++b, ++stage) {
           const uint32_t slot = stage % C::kStages, round = stage / C::kStages;
@@ -181,10 +225,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = false;
             break;
           }
-          uint8_t* W = smem + slot * C::kStageBytes;
-          mbar_expect_tx(&full[slot], C::kStageBytes);
-          tma_load_2d(W, &map_w, b * BK, tw * BM, &full[slot]);
-          tma_load_2d(W + BM * BK, &map_t, b * BK, tt * NT, &full[slot]);
+          uint8_t* T = smem + slot * C::kStageBytes;
+          mbar_expect_tx(&full[slot], (uint32_t)a.token_bytes + NT * BK);
+          tma_load_2d(T, &map_t, b * BK, tt * BM, &full[slot]);
+          tma_load_2d(T + BM * BK, &map_w, b * BK, tw * NT, &full[slot]);
         }
       }
       if (!ok) {  // let the copies already issued land before the CTA leaves
@@ -199,8 +243,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       const uint32_t smem0 = smem_u32(smem);
       for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-        int tw, tt, s;
-        unit_coords(u, a, tw, tt, s);
+        int tt, tw, s;
+        unit_coords(u, a, tt, tw, s);
         const int nb = min(a.kb, (s + 1) * a.kb_per_split) - s * a.kb_per_split;
         for (int b = 0; b < nb; ++b, ++stage) {
           const uint32_t buf = stage % C::kAccs, use = stage / C::kAccs;
@@ -211,12 +255,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           tc_fence_after();
-          // K-major rows of 128 bytes with the 128-byte swizzle; a step of 32 columns is 32 bytes
-          const uint64_t wd = sdesc_sw128(smem0 + slot * C::kStageBytes, 16, 1024);
-          const uint64_t td = sdesc_sw128(smem0 + slot * C::kStageBytes + BM * BK, 16, 1024);
+          // K-major rows of 128 bytes with the 128-byte swizzle; a step of 32 columns is 32 bytes.  Token rows
+          // that the box does not reach hold what was there before: they only reach accumulator rows
+          // that nobody reads.
+          const uint64_t td = sdesc_sw128(smem0 + slot * C::kStageBytes, 16, 1024);
+          const uint64_t wd = sdesc_sw128(smem0 + slot * C::kStageBytes + BM * BK, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            umma_f8(tmem_base + buf * NT, wd + (uint64_t)(kk * 2), td + (uint64_t)(kk * 2), a.idesc, kk > 0 ? 1u : 0u);
+            umma_f8(tmem_base + buf * NT, td + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), a.idesc, kk > 0 ? 1u : 0u);
           umma_commit(&empty[slot]);
           umma_commit(&acc_full[buf]);
         }
@@ -226,82 +272,121 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_wait_drain(drain, 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    const int ew = warp - 2;
-    const int quad = warp & 3;  // TMEM lanes this warp may access: 32*quad .. 32*quad+31
-    const int half = ew >> 2;   // tokens NT/2*half .. of the tile
-    const int et = threadIdx.x - 64;
-    constexpr int LD = C::kCols < 16 ? 8 : 16;  // TMEM columns per load
-    constexpr int TPT = (NT + EPI_WARPS * 32 - 1) / (EPI_WARPS * 32);  // tokens whose scales a thread stages
-    static_assert(TPT == 1, "one token per epilogue thread");
+    const int quad = warp & 3;         // TMEM lanes this warp may access: 32*quad .. 32*quad+31
+    const int part = (warp - 4) >> 2;  // columns kCols * part .. of the tile
+    const int et = threadIdx.x - 128;
+    const int r4 = lane >> 2, c4 = 2 * (lane & 3);  // this thread's rows r4 + 8 i and columns c4 + 8 j + {0, 1}
+    constexpr int J = 2;       // 8-column groups per load
+    constexpr int NQ = C::kCols / (8 * J);
+    constexpr int SR = C::kScaleRow;
     uint32_t stage = 0, group = 0;
     // After a wait that gave up the warp stops waiting and storing but still walks its units, because all
     // eight warps have to meet at the named barrier.
     bool ok = true;
     for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
-      int tw, tt, s;
-      unit_coords(u, a, tw, tt, s);
+      int tt, tw, s;
+      unit_coords(u, a, tt, tw, s);
       const int b0 = s * a.kb_per_split, b1 = min(a.kb, b0 + a.kb_per_split);
-      const int row = tw * BM + 32 * quad + lane;  // this thread's weight row
-      const int t0 = tt * NT;
-      const float* wsc = a.b_scales + (int64_t)(min(row, a.n - 1) >> a.b_shift) * a.kb;
-      const bool stages_scales = et < NT;
-      const float* tsc = a.a_scales + (int64_t)min(t0 + min(et, NT - 1), a.m - 1) * a.kb;
-      uint64_t acc[C::kCols / 2];
+      const int t0 = tt * BM, w0 = tw * NT;
+      // Scales are staged SG blocks at a time, one row and one column per thread.  BLOCK: the scale of the
+      // warp half's weight rows (they lie in one block of 128) times the token's; else the two apart.
+      const int st_half = et >> 7 & 1;
+      const float* tsc = a.a_scales + (int64_t)min(t0 + (et & 127), a.m - 1) * a.kb;
+      const float* wsc = BLOCK ? a.b_scales + (int64_t)(min(w0 + st_half * 128, a.n - 1) >> 7) * a.kb
+                               : a.b_scales + (int64_t)min(w0 + et, a.n - 1) * a.kb;
+      float t_next[SG], w_next[SG];  // the scales of the group to come
+      auto fetch = [&](int g0) {
+        if (BLOCK ? et < 2 * BM : et < BM) fetch_scales<SG>(tsc, g0, b1, a.vec_scales, t_next);
+        if (BLOCK ? et < 2 * BM : et < NT) fetch_scales<SG>(wsc, g0, b1, a.vec_scales, w_next);
+      };
+      fetch(b0);
+      const bool rows_here = t0 + 32 * quad < a.m;  // else the warp only keeps the barriers going
+      uint64_t acc[4][C::kCols / 8];  // [row r4 + 8 i][column group j]
 #pragma unroll
-      for (int c = 0; c < C::kCols / 2; ++c) acc[c] = 0ull;
-      float w_next = __ldg(wsc + b0);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < C::kCols / 8; ++j) acc[i][j] = 0ull;
       for (int g0 = b0; g0 < b1; g0 += SG, ++group) {
-        // the scales of this tile's tokens for SG blocks, [block][token]; the other buffer may still be read
-        float* sc = token_scales + (group & 1) * SG * NT;
-        if (stages_scales) {
+        float* sc = token_scales + (group & 1) * SG * SR;  // the other buffer may still be read
 #pragma unroll
-          for (int i = 0; i < SG; ++i) sc[i * NT + et] = g0 + i < b1 ? __ldg(tsc + g0 + i) : 0.0f;
+        for (int i = 0; i < SG; ++i) {
+          if (BLOCK) {
+            if (et < 2 * BM) sc[i * SR + et] = t_next[i] * w_next[i];  // [block of weight rows][token]
+          } else {
+            if (et < BM) sc[i * SR + et] = t_next[i];  // [token], then [weight row]
+            if (et < NT) sc[i * SR + BM + et] = w_next[i];
+          }
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
+        fetch(g0 + SG);
+        asm volatile("bar.sync 1, %0;" ::"n"(C::kEpiThreads) : "memory");
         const int g1 = min(b1, g0 + SG);
-        for (int b = g0; b < g1; ++b, ++stage) {
+        const float* rsc = sc + (BLOCK ? (part * C::kCols >> 7) * BM : 0) + 32 * quad + r4;
+        const float* csc = sc + BM + part * C::kCols + c4;
+        for (int b = g0; b < g1; ++b, ++stage, rsc += SR, csc += SR) {
           const uint32_t buf = stage % C::kAccs, use = stage / C::kAccs;
-          const float w = w_next;
-          if (b + 1 < b1) w_next = __ldg(wsc + b + 1);
-          const uint64_t w2 = pack2(__float_as_uint(w), __float_as_uint(w));
-          const float* scb = sc + (b - g0) * NT + half * C::kCols;
+          uint64_t rs[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v = __float_as_uint(rsc[8 * i]);
+            rs[i] = pack2(v, v);
+          }
           if (ok) ok = mbar_wait(&acc_full[buf], use & 1, abort_flag, a.status, 54);
           tc_fence_after();
-          const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * NT + half * C::kCols;
+          const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * NT + part * C::kCols;
+          if (!rows_here) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            continue;
+          }
+          // the next columns are on their way from TMEM while these are added
+          uint32_t v[2][2][4 * J];  // [buffer][16-row half]
+          tmem_ld<J>(taddr, v[0][0]);
+          tmem_ld<J>(taddr + (16u << 16), v[0][1]);
 #pragma unroll
-          for (int q = 0; q < C::kCols / LD; ++q) {
-            uint32_t v[LD];
-            tmem_ld<LD>(taddr + LD * q, v);
+          for (int q = 0; q < NQ; ++q) {
             tmem_wait();
+            if (q + 1 < NQ) {
+              tmem_ld<J>(taddr + 8 * J * (q + 1), v[(q + 1) & 1][0]);
+              tmem_ld<J>(taddr + 8 * J * (q + 1) + (16u << 16), v[(q + 1) & 1][1]);
+            } else {  // the last columns are in registers: the accumulator goes back to the MMAs
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            }
 #pragma unroll
-            for (int i = 0; i < LD; i += 4) {
-              const ulonglong2 ts = *reinterpret_cast<const ulonglong2*>(scb + LD * q + i);
-              const int c = (LD * q + i) / 2;
-              acc[c] = fma2(mul2(pack2(v[i], v[i + 1]), ts.x), w2, acc[c]);
-              acc[c + 1] = fma2(mul2(pack2(v[i + 2], v[i + 3]), ts.y), w2, acc[c + 1]);
+            for (int j = 0; j < J; ++j) {
+              uint64_t cs = 0;
+              if constexpr (!BLOCK) cs = *reinterpret_cast<const uint64_t*>(csc + 8 * (J * q + j));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t* p = &v[q & 1][i >> 1][4 * j + 2 * (i & 1)];
+                const uint64_t pp = pack2(p[0], p[1]);
+                acc[i][J * q + j] = fma2(BLOCK ? pp : mul2(pp, cs), rs[i], acc[i][J * q + j]);
+              }
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
       }
-      if (ok && row < a.n) {
-        const int tok0 = t0 + half * C::kCols;
+      if (ok && rows_here) {
+        const bool even = (a.n & 1) == 0;  // rows start on pairs
 #pragma unroll
-        for (int c = 0; c < C::kCols; c += 2) {
-          float v0, v1;
-          unpack2(acc[c / 2], v0, v1);
-          if (a.partial == nullptr) {
-            TY* y = static_cast<TY*>(a.Y) + (int64_t)(tok0 + c) * a.n + row;
-            if (tok0 + c < a.m) y[0] = from_f32<TY>(v0);
-            if (tok0 + c + 1 < a.m) y[a.n] = from_f32<TY>(v1);
-          } else {
-            float* y = a.partial + ((int64_t)s * a.m + tok0 + c) * a.n + row;
-            if (tok0 + c < a.m) y[0] = v0;
-            if (tok0 + c + 1 < a.m) y[a.n] = v1;
+        for (int i = 0; i < 4; ++i) {
+          const int tok = t0 + 32 * quad + r4 + 8 * i;
+          if (tok >= a.m) continue;
+          const int w = w0 + part * C::kCols + c4;
+          const int64_t at = ((int64_t)s * (a.partial ? a.m : 0) + tok) * a.n + w;
+#pragma unroll
+          for (int j = 0; j < C::kCols / 8; ++j) {
+            float v0, v1;
+            unpack2(acc[i][j], v0, v1);
+            const int left = a.n - w - 8 * j;
+            if (a.partial == nullptr)
+              store_pair(static_cast<TY*>(a.Y) + at + 8 * j, v0, v1, left, even && left > 1);
+            else
+              store_pair(a.partial + at + 8 * j, v0, v1, left, even && left > 1);
           }
         }
       }
@@ -313,6 +398,342 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// CTA-pair form, for products with enough 256 x 256 tiles to fill the GPU.  A cluster of two CTAs computes
+// a tile of 256 tokens x 256 weight rows with tcgen05.mma.cta_group::2: each CTA loads its 128 tokens and
+// half of the weight rows (32 KB per block, where the single-CTA tile of the same area per SM takes 48 KB
+// in and out of shared memory and out of L2).  The tile's columns are two accumulators of 128, each with
+// its own barriers and its own four epilogue warps, double-buffered: while one half's warps read their
+// sums the MMAs of the other half run, and the two warps of a scheduler wait at different times.
+//   BLOCK: a thread holds one token row (32x32b loads), one scale per thread and block
+//   else:  four token rows and column pairs (16x256b loads), the weights' scales from shared memory
+constexpr int PN = 256;                           // weight rows of a pair's tile
+constexpr int P_STAGES = 5;
+constexpr int P_STAGE_BYTES = (BM + PN / 2) * BK;  // per CTA
+constexpr int P_EPI_WARPS = 8;
+constexpr int P_THREADS = 128 + P_EPI_WARPS * 32;
+constexpr int P_SG = 4;                            // blocks whose scales are staged at a time
+constexpr int P_SCALE_ROW = 2 * BM;                // floats per block and half: tokens, then its weight rows
+constexpr int P_SCALE_BYTES = 2 * 2 * P_SG * P_SCALE_ROW * 4;  // [half][buffer][block]
+constexpr int P_OUT_BYTES = P_EPI_WARPS * 4096;    // a 32-row x 128-byte tile per warp on its way to Y
+constexpr int P_SMEM = P_STAGES * P_STAGE_BYTES + P_OUT_BYTES + P_SCALE_BYTES + 1024 + 512;
+// register split (per thread): warps 0-3 give theirs up to the epilogue, whose sums take 128
+constexpr int kLaunchRegs = 168, kEpiRegs = 232, kOtherRegs = 40;
+static_assert(128 * kOtherRegs + P_EPI_WARPS * 32 * kEpiRegs <= P_THREADS * kLaunchRegs, "register split");
+static_assert(P_SMEM <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void umma_f8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 16 consecutive TMEM columns of this warp's 32 lanes; there after tmem_wait()
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Arrive on an accumulator's barrier of either CTA.  Relaxed: the sums are in registers (tcgen05.wait::ld) and
+// nothing else is handed over; the releasing form waits for the warp's memory accesses at cluster scope
+// every time (the membar stall then led all others, 831 us for the product below).
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Every warp of both CTAs, before any of them leaves: the pair's MMAs are done and no arrival is on its way to
+// the other CTA.  (Met from both sides of the register split, whose code must not join again.)
+__device__ __forceinline__ void pair_exit_barrier() {
+  __syncwarp();
+  asm volatile("bar.sync 0, %0;" ::"n"(P_THREADS) : "memory");
+  cluster_sync();
+}
+
+template <bool BLOCK, typename TY>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
+                           const __grid_constant__ CUtensorMap map_y, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* out_tiles = smem + P_STAGES * P_STAGE_BYTES;
+  float* staged = reinterpret_cast<float*>(out_tiles + P_OUT_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_tiles + P_OUT_BYTES + P_SCALE_BYTES);
+  uint64_t* empty = full + P_STAGES;
+  uint64_t* acc_full = empty + P_STAGES;  // [buffer][half]
+  uint64_t* acc_empty = acc_full + 4;
+  uint64_t* drain = acc_empty + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();  // 0 leads the pair
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 2);  // both issuers are through with the stage
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], P_EPI_WARPS);  // four warps of each CTA
+    }
+    mbar_init(drain, 2);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any arrival crosses the pair
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer (this CTA's halves)
+      if (lane == 0) {
+        uint32_t stage = 0;
+        bool ok = true;
+        const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's stage barriers
+        for (int u = pair; u < a.units && ok; u += n_pairs) {
+          int tt, tw, s;
+          unit_coords(u, a, tt, tw, s);
+          for (int b = 0; b < a.kb; ++b, ++stage) {
+            const uint32_t slot = stage % P_STAGES, round = stage / P_STAGES;
+            if (!mbar_wait(&empty[slot], (round & 1) ^ 1, abort_flag, a.status, 61)) {
+              ok = false;
+              break;
+            }
+            uint8_t* T = smem + slot * P_STAGE_BYTES;
+            const uint32_t bar = full0 + slot * 8;
+            if (rank == 0) mbar_expect_tx(&full[slot], 2 * P_STAGE_BYTES);
+            tma_load_2d_pair(T, &map_t, b * BK, tt * 2 * BM + BM * (int)rank, bar);
+            // of each half's 128 weight rows, this CTA's 64
+            tma_load_2d_pair(T + BM * BK, &map_w, b * BK, tw * PN + 64 * (int)rank, bar);
+            tma_load_2d_pair(T + BM * BK + 64 * BK, &map_w, b * BK, tw * PN + 128 + 64 * (int)rank, bar);
+          }
+        }
+        // the copies already issued land before the CTA leaves: the even CTA watches both CTAs' on its stage
+        // barriers, and the cluster barrier at the end keeps the odd CTA resident until then
+        if (!ok && rank == 0) {
+          const uint32_t first = stage > P_STAGES ? stage - P_STAGES : 0;
+          for (uint32_t i = first; i < stage; ++i) mbar_wait_drain_cluster(&full[i % P_STAGES], (i / P_STAGES) & 1);
+        }
+      }
+    } else if (warp == 1 || warp == 2) {
+      if (lane == 0 && rank == 0) {
+        // -------------------------------------------------------------- MMA issuers (even CTA), one per half
+        const int h = warp - 1;
+        uint32_t stage = 0;
+        bool ok = true;
+        const uint64_t desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t w_off = (uint64_t)((BM * BK + h * 64 * BK) >> 4);
+        for (int u = pair; u < a.units && ok; u += n_pairs) {
+          for (int b = 0; b < a.kb; ++b, ++stage) {
+            const uint32_t slot = stage % P_STAGES, round = stage / P_STAGES, buf = stage & 1, use = stage >> 1;
+            if (!mbar_wait(&acc_empty[2 * buf + h], (use & 1) ^ 1, abort_flag, a.status, 62) ||
+                !mbar_wait(&full[slot], round & 1, abort_flag, a.status, 63)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t td = desc0 + (uint64_t)((slot * P_STAGE_BYTES) >> 4);
+  #pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              umma_f8_pair(tmem_base + (2 * buf + h) * 128, td + (uint64_t)(kk * 2), td + w_off + (uint64_t)(kk * 2),
+                           a.idesc, kk > 0 ? 1u : 0u);
+            umma_commit_pair(&acc_full[2 * buf + h]);
+            umma_commit_pair(&empty[slot]);
+          }
+        }
+        // every MMA of the pair is complete before either CTA frees TMEM or leaves
+        umma_commit_pair(drain);
+        mbar_wait_drain(drain, 0);
+      } else if (lane == 0) {
+        mbar_wait_drain(drain, 0);  // odd CTA: the pair's last MMAs are complete
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    pair_exit_barrier();
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc_pair(tmem_base, 512);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue (this CTA's tokens)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int quad = warp & 3;
+    const int half = (warp - 4) >> 2;  // columns 128 * half .. of the tile
+    const int et = threadIdx.x & 127;  // this thread among the half's 128
+    const int r4 = lane >> 2, c4 = 2 * (lane & 3);
+    const uint32_t acc_empty0 = mapa_shared(acc_empty, 0);
+    uint8_t* out_tile = out_tiles + (warp - 4) * 4096;
+    uint32_t stage = 0, group = 0;
+    bool ok = true;  // as in the single-CTA kernel: no warp leaves the walk, the named barrier needs all
+    for (int u = pair; u < a.units; u += n_pairs) {
+      int tt, tw, s;
+      unit_coords(u, a, tt, tw, s);
+      const int t0 = tt * 2 * BM + BM * (int)rank, w0 = tw * PN + 128 * half;
+      // scales staged P_SG blocks at a time, each half its own; BLOCK: the tokens' times the weight rows' one
+      const float* tsc = a.a_scales + (int64_t)min(t0 + et, a.m - 1) * a.kb;
+      const float* wsc = BLOCK ? a.b_scales + (int64_t)(min(w0, a.n - 1) >> 7) * a.kb
+                               : a.b_scales + (int64_t)min(w0 + et, a.n - 1) * a.kb;
+      float t_next[P_SG], w_next[P_SG];
+      auto fetch = [&](int g0) {
+        fetch_scales<P_SG>(tsc, g0, a.kb, a.vec_scales, t_next);
+        fetch_scales<P_SG>(wsc, g0, a.kb, a.vec_scales, w_next);
+      };
+      fetch(0);
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      for (int g0 = 0; g0 < a.kb; g0 += P_SG, ++group) {
+        float* sc = staged + (half * 2 + (group & 1)) * P_SG * P_SCALE_ROW;  // the other buffer may still be read
+#pragma unroll
+        for (int i = 0; i < P_SG; ++i) {
+          sc[i * P_SCALE_ROW + et] = BLOCK ? t_next[i] * w_next[i] : t_next[i];
+          if (!BLOCK) sc[i * P_SCALE_ROW + BM + et] = w_next[i];
+        }
+        fetch(g0 + P_SG);
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+        const int g1 = min(a.kb, g0 + P_SG);
+        for (int b = g0; b < g1; ++b, ++stage, sc += P_SCALE_ROW) {
+          const uint32_t buf = stage & 1, use = stage >> 1;
+          const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + (2 * buf + half) * 128;
+          if constexpr (BLOCK) {
+            const uint32_t rs1 = __float_as_uint(sc[32 * quad + lane]);
+            const uint64_t rs = pack2(rs1, rs1);
+            if (ok) ok = mbar_wait(&acc_full[2 * buf + half], use & 1, abort_flag, a.status, 66);
+            tc_fence_after();
+            uint32_t v[2][16];
+            tmem_ld_rows(taddr, v[0]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              tmem_wait();
+              if (q < 7) {  // the next columns are on their way from TMEM while these are added
+                tmem_ld_rows(taddr + 16 * (q + 1), v[(q + 1) & 1]);
+              } else {      // the last columns are in registers: the accumulator goes back to the MMAs
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(acc_empty0 + (2 * buf + half) * 8);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                acc[8 * q + i] = fma2(pack2(v[q & 1][2 * i], v[q & 1][2 * i + 1]), rs, acc[8 * q + i]);
+            }
+          } else {
+            uint64_t rs[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t v = __float_as_uint(sc[32 * quad + r4 + 8 * i]);
+              rs[i] = pack2(v, v);
+            }
+            const float* csc = sc + BM + c4;
+            if (ok) ok = mbar_wait(&acc_full[2 * buf + half], use & 1, abort_flag, a.status, 66);
+            tc_fence_after();
+            uint32_t v[2][8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              tmem_ld<2>(taddr + 16 * q, v[0]);
+              tmem_ld<2>(taddr + 16 * q + (16u << 16), v[1]);
+              const uint64_t cs[2] = {*reinterpret_cast<const uint64_t*>(csc + 16 * q),
+                                      *reinterpret_cast<const uint64_t*>(csc + 16 * q + 8)};
+              tmem_wait();
+              if (q == 7) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(acc_empty0 + (2 * buf + half) * 8);
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t* p = &v[i >> 1][4 * j + 2 * (i & 1)];
+                  acc[16 * i + 2 * q + j] = fma2(mul2(pack2(p[0], p[1]), cs[j]), rs[i], acc[16 * i + 2 * q + j]);
+                }
+            }
+          }
+        }
+      }
+      if (!ok) continue;
+      const int row0 = t0 + 32 * quad;
+      if (a.vec_y) {
+        // through shared memory as 32 rows x 128 bytes (16-byte chunks swizzled by the row, as the copy
+        // expects), then asynchronously to Y; what lies past Y's edges is not written.  Stores straight
+        // from the registers were 16 bytes of 32 rows at a time and cost 160 us of the product's 557.
+        constexpr int OC = 128 / (int)sizeof(TY);  // columns per tile
+#pragma unroll
+        for (int o = 0; o < 128 / OC; ++o) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          if constexpr (BLOCK) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              constexpr int V = 16 / (int)sizeof(TY);
+              TY h[V];
+#pragma unroll
+              for (int i = 0; i < V; i += 2) {
+                float v0, v1;
+                unpack2(acc[(o * OC + c * V + i) / 2], v0, v1);
+                h[i] = from_f32<TY>(v0), h[i + 1] = from_f32<TY>(v1);
+              }
+              *reinterpret_cast<uint4*>(out_tile + lane * 128 + ((c ^ (lane & 7)) << 4)) = *reinterpret_cast<uint4*>(h);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < OC / 8; ++j) {
+                float v0, v1;
+                unpack2(acc[16 * i + o * (OC / 8) + j], v0, v1);
+                const int byte = (8 * j + c4) * (int)sizeof(TY);
+                TY* y = reinterpret_cast<TY*>(out_tile + (r4 + 8 * i) * 128 + ((byte >> 4 ^ r4) << 4) + (byte & 15));
+                store_pair(y, v0, v1, 2, true);
+              }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row0 < a.m && w0 + o * OC < a.n) {
+            tma_store_2d(&map_y, w0 + o * OC, row0, out_tile);
+            bulk_commit();
+          }
+        }
+      } else if constexpr (BLOCK) {
+        if (row0 + lane < a.m && w0 < a.n)
+          store_row<128>(acc, static_cast<TY*>(a.Y) + (int64_t)(row0 + lane) * a.n + w0, a.n - w0);
+      } else {
+        const bool even = (a.n & 1) == 0;  // rows start on pairs
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = row0 + r4 + 8 * i, w = w0 + c4;
+          if (tok >= a.m) continue;
+          TY* y = static_cast<TY*>(a.Y) + (int64_t)tok * a.n + w;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float v0, v1;
+            unpack2(acc[16 * i + j], v0, v1);
+            const int left = a.n - w - 8 * j;
+            store_pair(y + 8 * j, v0, v1, left, even && left > 1);
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait<0>();  // the copies to Y are complete
+    tc_fence_before();
+    pair_exit_barrier();
   }
 }
 
@@ -328,31 +749,38 @@ __global__ void __launch_bounds__(256) fp8_matmul_reduce_kernel(const float* __r
 }
 
 struct Plan {
-  int nt, tiles_w, tiles_t, kb, kb_per_split, splits;
+  int nt, tiles_t, tiles_w, kb, kb_per_split, splits;  // nt = 256: the pair form
 };
 
-// Tile width and split of the blocks with the lowest estimated time in cycles: a block costs an SM about
-// 330 + 2.6 NT (its operands' way through shared memory), a unit 1500 for its fill and its epilogue, and
-// split sums are written and read back at about 3000 bytes per cycle of the whole GPU plus a launch.
+// Form, tile width and split of the blocks with the lowest estimated time in cycles: a block costs an SM
+// 256 + 2 NT (its operands' way into and out of shared memory), a unit 1500 for its fill and its epilogue,
+// and split sums are written and read back at about 3000 bytes per cycle of the whole GPU plus a launch.
 Plan make_plan(int64_t m, int64_t n, int64_t k) {
   Plan best = {};
   double best_cost = 1e300;
   const int kb = (int)((k + BK - 1) / BK);
-  for (int nt = 16; nt <= 256; nt *= 2) {
-    const int64_t tw = (n + BM - 1) / BM, tt = (m + nt - 1) / nt;
+  // splits start on multiples of 4 blocks so that their scales' 16-byte loads stay aligned
+  for (int nt = 32; nt <= 128; nt *= 2) {
+    const int64_t tw = (n + nt - 1) / nt, tt = (m + BM - 1) / BM;
     for (int want = 1; want <= 16 && want <= kb; ++want) {
-      const int per = (kb + want - 1) / want, splits = (kb + per - 1) / per;
+      const int per = want == 1 ? kb : ((kb + want - 1) / want + 3) / 4 * 4, splits = (kb + per - 1) / per;
       if (splits != want) continue;
       const int64_t units = tw * tt * splits;
       if (splits > 1 && units > 2 * kPlanSMs) continue;
       const double waves = (double)((units + kPlanSMs - 1) / kPlanSMs);
-      double cost = waves * (per * (330.0 + 2.6 * nt) + 1500.0);
+      double cost = waves * (per * (256.0 + 2.0 * nt) + 1500.0);
       if (splits > 1) cost += 8.0 * splits * (double)m * (double)n / 3000.0 + 4000.0;
       if (cost < best_cost) {
         best_cost = cost;
-        best = {nt, (int)tw, (int)tt, kb, per, splits};
+        best = {nt, (int)tt, (int)tw, kb, per, splits};
       }
     }
+  }
+  if (m > BM) {
+    const int64_t tw = (n + PN - 1) / PN, tt = (m + 2 * BM - 1) / (2 * BM);
+    const double waves = (double)((tw * tt + kPlanSMs / 2 - 1) / (kPlanSMs / 2));
+    const double cost = waves * (kb * 800.0 + 4000.0);
+    if (cost < best_cost) best = {PN, (int)tt, (int)tw, kb, kb, 1};
   }
   return best;
 }
@@ -370,27 +798,64 @@ bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, typename TY>
-gptq_status launch(const CUtensorMap& w, const CUtensorMap& t, Args a, int sms, cudaStream_t s) {
+// Y in tiles of 32 rows x 128 bytes with the 128-byte swizzle
+template <typename TY>
+bool out_map(CUtensorMap* map, void* base, int64_t m, int64_t n) {
+  auto encode = encode_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)m};
+  const cuuint64_t strides[1] = {(cuuint64_t)(n * sizeof(TY))};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(TY)), 32};
+  const cuuint32_t elem[2] = {1, 1};
+  const CUtensorMapDataType type = std::is_same<TY, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : std::is_same<TY, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return encode(map, type, 2, base, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+template <int NT, bool BLOCK, typename TY>
+gptq_status launch(const CUtensorMap& t, const CUtensorMap& w, Args a, int sms, cudaStream_t s) {
+  auto kernel = fp8_matmul_kernel<NT, BLOCK, TY>;
   // D fp32 (bit 4), A and B e4m3 (0), both K-major, N = NT, M = 128
   a.idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-  GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_matmul_kernel<NT, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Cfg<NT>::kSmem));
-  fp8_matmul_kernel<NT, TY><<<std::min(a.units, sms), THREADS, Cfg<NT>::kSmem, s>>>(w, t, a);
+  GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmem));
+  kernel<<<std::min(a.units, sms), Cfg<NT>::kThreads, Cfg<NT>::kSmem, s>>>(t, w, a);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
+template <bool BLOCK, typename TY>
+gptq_status launch_pair(const CUtensorMap& t, const CUtensorMap& w, Args a, int sms, cudaStream_t s) {
+  CUtensorMap y = t;  // not used unless Y's rows are aligned
+  if (a.vec_y && !out_map<TY>(&y, a.Y, a.m, a.n)) return GPTQ_ERR_CUDA;
+  auto kernel = fp8_matmul_pair_kernel<BLOCK, TY>;
+  a.idesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)((2 * BM) >> 4) << 24);
+  cudaFuncAttributes attr;  // the register split draws on the launch's registers: never ask for more than those
+  GPTQ_CUDA_TRY(cudaFuncGetAttributes(&attr, kernel));
+  if (attr.numRegs < kLaunchRegs) return GPTQ_ERR_CUDA;
+  GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM));
+  kernel<<<2 * std::min(a.units, sms / 2), P_THREADS, P_SMEM, s>>>(t, w, y, a);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+template <int NT, typename TY>
+gptq_status launch_block(bool block, const CUtensorMap& t, const CUtensorMap& w, const Args& a, int sms,
+                         cudaStream_t s) {
+  return block ? launch<NT, true, TY>(t, w, a, sms, s) : launch<NT, false, TY>(t, w, a, sms, s);
+}
+
 template <typename TY>
-gptq_status launch_typed(const Plan& p, const CUtensorMap& w, const CUtensorMap& t, const Args& a, int sms,
+gptq_status launch_typed(const Plan& p, bool block, const CUtensorMap& t, const CUtensorMap& w, const Args& a, int sms,
                          cudaStream_t s) {
   gptq_status st;
   switch (p.nt) {
-    case 16: st = launch<16, TY>(w, t, a, sms, s); break;
-    case 32: st = launch<32, TY>(w, t, a, sms, s); break;
-    case 64: st = launch<64, TY>(w, t, a, sms, s); break;
-    case 128: st = launch<128, TY>(w, t, a, sms, s); break;
-    default: st = launch<256, TY>(w, t, a, sms, s); break;
+    case 32: st = launch_block<32, TY>(block, t, w, a, sms, s); break;
+    case 64: st = launch_block<64, TY>(block, t, w, a, sms, s); break;
+    case 128: st = launch_block<128, TY>(block, t, w, a, sms, s); break;
+    default: st = block ? launch_pair<true, TY>(t, w, a, sms, s) : launch_pair<false, TY>(t, w, a, sms, s); break;
   }
   if (st != GPTQ_OK || a.partial == nullptr) return st;
   const int64_t e = (int64_t)a.m * a.n;
@@ -413,8 +878,9 @@ gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* 
   const Plan p = make_plan(m, n, k);
   const int64_t units = (int64_t)p.tiles_w * p.tiles_t * p.splits;
   if (units > 0x7fffffff - kPlanSMs) return GPTQ_ERR_ARG;
-  CUtensorMap w, t;
-  if (!operand_map(&w, B, n, k, BM) || !operand_map(&t, A, m, k, p.nt)) return GPTQ_ERR_CUDA;
+  const int token_rows = (int)std::min<int64_t>(BM, (m + 7) / 8 * 8);  // whole swizzle atoms of 8 rows
+  CUtensorMap t, w;
+  if (!operand_map(&t, A, m, k, token_rows) || !operand_map(&w, B, n, k, p.nt == PN ? 64 : p.nt)) return GPTQ_ERR_CUDA;
   int dev = 0, sms = 0;
   GPTQ_CUDA_TRY(cudaGetDevice(&dev));
   GPTQ_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -422,15 +888,18 @@ gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* 
   a.m = (int)m, a.n = (int)n, a.kb = p.kb;
   a.tiles_w = p.tiles_w, a.tiles_t = p.tiles_t, a.units = (int)units;
   a.kb_per_split = p.kb_per_split;
-  a.b_shift = b_block_rows == 128 ? 7 : 0;
+  a.token_bytes = token_rows * BK;
+  a.vec_scales = p.kb % 4 == 0 && aligned(a_scales, 16) && aligned(b_scales, 16);
+  a.vec_y = n * (y_dtype == GPTQ_FP32 ? 4 : 2) % 16 == 0 && aligned(Y, 16);
+  const bool block = b_block_rows == 128;
   a.a_scales = a_scales, a.b_scales = b_scales;
   a.Y = Y;
   a.partial = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   a.status = status;
   switch (y_dtype) {
-    case GPTQ_BF16: return launch_typed<__nv_bfloat16>(p, w, t, a, sms, stream);
-    case GPTQ_FP16: return launch_typed<__half>(p, w, t, a, sms, stream);
-    default: return launch_typed<float>(p, w, t, a, sms, stream);
+    case GPTQ_BF16: return launch_typed<__nv_bfloat16>(p, block, t, w, a, sms, stream);
+    case GPTQ_FP16: return launch_typed<__half>(p, block, t, w, a, sms, stream);
+    default: return launch_typed<float>(p, block, t, w, a, sms, stream);
   }
 }
 
