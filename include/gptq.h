@@ -15,7 +15,8 @@
  *
  * Conventions shared by every entry point:
  *  - Matrices are dense and row-major with no padding (leading dimension = number of columns).
- *  - Every pointer argument except `cfg` and `detail` is DEVICE memory on the current CUDA device,
+ *  - Every pointer argument except `cfg`, `detail` and the gptq_moe_weights structures (whose members are
+ *    device pointers) is DEVICE memory on the current CUDA device,
  *    allocated and owned by the caller.  The library allocates no device or host memory and keeps no
  *    state between calls (apart from a cached driver entry point).
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Every call only enqueues work on
@@ -324,6 +325,57 @@ GPTQ_API gptq_status gptq_fp8_matmul(const void* A, const float* a_scales, const
                                      int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* Y, int32_t y_dtype,
                                      int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
 GPTQ_API size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* ------------------------------------------------------------------------------------------
+ * A mixture-of-experts layer for a few tokens over packed weights (the products of gptq_dequant_matmul for
+ * the experts that a router chooses, in one call):
+ *   l = X router^T;  p = softmax(l);  e_1 .. e_K = the top_k largest p (largest first, ties to the lowest
+ *   index);  w_i = p[e_i], divided by their sum with GPTQ_MOE_RENORMALIZE
+ *   Y[t] = sum_i w_i * Down_{e_i} a_i,   a_i = silu(Gate_{e_i} x) * (Up_{e_i} x)   (GPTQ_ACT_SILU_GATED)
+ *                                        a_i = max(Up_{e_i} x, 0)                  (GPTQ_ACT_RELU)
+ * where every expert's matrix stands for scale[r, g(j)] * (q[r, j] - zero[r, g(j)]).
+ *
+ *   X            [tokens, d], BF16 / FP16 / FP32, 16-byte aligned; 0 <= tokens <= 64.
+ *   router       [n_experts, d] in X's type, 16-byte aligned; or NULL: the caller's own routing is read from
+ *                topk_ids and topk_weights.
+ *   up, gate     n_experts matrices [f, d] one behind the other: packed [n_experts, f, d*bits/32] int32
+ *                (gptq_pack), 16-byte aligned; scales / zeros [n_experts, f, n_groups], zeros in [0, 2^bits - 1]
+ *                as gptq_quantize_layer writes them.  gate: all NULL with GPTQ_ACT_RELU.
+ *   down         n_experts matrices [d, f] likewise.
+ *   topk_ids     int32 [tokens, top_k], topk_weights fp32 [tokens, top_k]: outputs with a router, inputs
+ *                without.  As inputs the same expert may be given twice; an id outside [0, n_experts) is recorded
+ *                as {GPTQ_ERR_ARG, its place} in dev_status and adds nothing.
+ *   Y            [tokens, d] in y_dtype, rounded once from the fp32 sum.
+ *   dev_status   int32[2], zeroed by the caller once, not cleared by the call.
+ *   workspace    >= gptq_moe_workspace_size(tokens, d, f, n_experts, top_k) bytes, 256-byte aligned.  Calls that may
+ *                overlap on the GPU, captured graphs among them, each need their own.
+ *   d % 32 == 0, f % 32 == 0; d, f <= 2^20; 1 <= n_experts <= 256; 1 <= top_k <= min(n_experts, 16) (without a
+ *   router top_k <= 16); bits in {2, 3, 4}; group_size 0 or a multiple of 32 that divides d and f.
+ *   Under act-order the packed codes are in the quantization order and X's (and a_i's) columns have to be
+ *   permuted alike, which this call does not do.
+ * Products q x are exact (X is split into bf16 terms that add up to it; a_i stays in fp32 and is split into three,
+ * or into two where Y has 16 bits), sums fp32 and in a fixed order: results are deterministic.
+ * ------------------------------------------------------------------------------------------ */
+#define GPTQ_ACT_SILU_GATED 0
+#define GPTQ_ACT_RELU 1
+#define GPTQ_MOE_RENORMALIZE 1u
+typedef struct {
+  int32_t n_experts, top_k;
+  int32_t bits, group_size;  /* of all matrices */
+  int32_t activation;        /* GPTQ_ACT_* */
+  uint32_t flags;            /* GPTQ_MOE_* */
+} gptq_moe_cfg;
+typedef struct {             /* one matrix per expert, device pointers */
+  const int32_t* packed;
+  const float* scales;
+  const int32_t* zeros;
+} gptq_moe_weights;
+GPTQ_API gptq_status gptq_moe_layer(const void* X, int32_t x_dtype, int64_t tokens, int64_t d, int64_t f,
+                                    const gptq_moe_cfg* cfg, const void* router, const gptq_moe_weights* up,
+                                    const gptq_moe_weights* gate, const gptq_moe_weights* down, int32_t* topk_ids,
+                                    float* topk_weights, void* Y, int32_t y_dtype, int32_t* dev_status,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+GPTQ_API size_t gptq_moe_workspace_size(int64_t tokens, int64_t d, int64_t f, int64_t n_experts, int64_t top_k);
 
 /* ------------------------------------------------------------------------------------------
  * Status helpers.

@@ -15,6 +15,7 @@ and the calls that answer with the result:
 
     Y = X What^T, a few rows          gptq_dequant_matmul   (packed codes)
     Y = X What^T, many rows           gptq_fp8_from_packed once, then gptq_fp8_quantize + gptq_fp8_matmul
+    mixture of experts, a few tokens  gptq_moe_layer        (packed codes)
 
 ``LayerSolver`` strings the four calls together over preallocated buffers.
 """
@@ -32,6 +33,7 @@ __all__ = [
     "gptq_act_order", "gptq_quantize_layer_act_order", "gptq_quantize_act_order_workspace_size", "act_order_group_index",
     "gptq_dequant_matmul", "gptq_dequant_matmul_workspace_size", "gptq_dequantize",
     "gptq_fp8_quantize", "gptq_fp8_from_packed", "gptq_fp8_matmul", "gptq_fp8_matmul_workspace_size",
+    "gptq_moe_layer", "gptq_moe_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
@@ -44,6 +46,19 @@ GPTQ_FLAG_FP32_FMA = 2
 GPTQ_TC_HESSIAN, GPTQ_TC_PREPARE, GPTQ_TC_LAZY = 1, 2, 4
 
 _DTYPES = {torch.bfloat16: GPTQ_BF16, torch.float16: GPTQ_FP16, torch.float32: GPTQ_FP32}
+
+
+GPTQ_ACT_SILU_GATED, GPTQ_ACT_RELU = 0, 1
+GPTQ_MOE_RENORMALIZE = 1
+
+
+class MoeCfg(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("bits", ctypes.c_int32),
+                ("group_size", ctypes.c_int32), ("activation", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class MoeWeights(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
 class QuantCfg(ctypes.Structure):
@@ -75,6 +90,10 @@ ABI_FUNCTIONS = {
     "gptq_fp8_from_packed": (_i32, [_vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
     "gptq_fp8_matmul": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _sz, _vp]),
     "gptq_fp8_matmul_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "gptq_moe_layer": (_i32, [_vp, _i32, _i64, _i64, _i64, ctypes.POINTER(MoeCfg), _vp, ctypes.POINTER(MoeWeights),
+                              ctypes.POINTER(MoeWeights), ctypes.POINTER(MoeWeights), _vp, _vp, _vp, _i32, _vp, _vp, _sz,
+                              _vp]),
+    "gptq_moe_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "gptq_read_status": (_i32, [_vp, _vp, ctypes.POINTER(_i64)]),
     "gptq_status_string": (ctypes.c_char_p, [_i32]),
     "gptq_abi_version": (_i32, []),
@@ -349,6 +368,53 @@ def gptq_fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_
         _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), b_block_rows, m, n, k, _ptr(Y), _DTYPES[Y.dtype],
         _ptr(status), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
     _check(st, "gptq_fp8_matmul")
+
+
+# ------------------------------------------------------------------------------------------ mixture of experts
+def gptq_moe_workspace_size(tokens: int, d: int, f: int, n_experts: int, top_k: int) -> int:
+    return lib().gptq_moe_workspace_size(tokens, d, f, n_experts, top_k)
+
+
+def gptq_moe_layer(X: torch.Tensor, router: torch.Tensor | None, up: tuple, gate: tuple | None, down: tuple,
+                   topk_ids: torch.Tensor, topk_weights: torch.Tensor, Y: torch.Tensor, status: torch.Tensor,
+                   workspace: torch.Tensor, bits: int, group_size: int = 0, activation: int = GPTQ_ACT_SILU_GATED,
+                   flags: int = 0, stream=None):
+    """Y [tokens, d] = the mixture-of-experts layer of X [tokens, d] over packed experts, for up to 64 tokens.
+
+    ``up``, ``gate`` (None with GPTQ_ACT_RELU) and ``down`` are (packed, scales, zeros) of all experts: packed
+    [n_experts, f, d*bits/32] for up and gate, [n_experts, d, f*bits/32] for down.  ``router`` [n_experts, d] in X's
+    type fills topk_ids and topk_weights [tokens, top_k]; without one they are the routing to use."""
+    tokens, d = X.shape
+    dev, dt = X.device, X.dtype
+    top_k = topk_ids.shape[1]
+    if bits not in (2, 3, 4) or group_size < 0:
+        raise ValueError(f"bits {bits}, group_size {group_size}")
+    experts, f = up[0].shape[0], up[0].shape[1]
+
+    def matrices(w, name, rows, cols):
+        ng = cols // group_size if group_size else 1
+        _shaped(w[0], name + " packed", (experts, rows, cols * bits // 32), torch.int32, dev)
+        _shaped(w[1], name + " scales", (experts, rows, ng), torch.float32, dev)
+        _shaped(w[2], name + " zeros", (experts, rows, ng), torch.int32, dev)
+        return MoeWeights(*(t.data_ptr() for t in w))
+
+    _shaped(X, "X", (tokens, d), _DTYPES, dev)
+    if router is not None:
+        _shaped(router, "router", (experts, d), dt, dev)
+    _shaped(topk_ids, "topk_ids", (tokens, top_k), torch.int32, dev)
+    _shaped(topk_weights, "topk_weights", (tokens, top_k), torch.float32, dev)
+    _shaped(Y, "Y", (tokens, d), _DTYPES, dev)
+    _shaped(status, "status", (2,), torch.int32, dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    u, w = matrices(up, "up", f, d), matrices(down, "down", d, f)
+    g = None if gate is None else matrices(gate, "gate", f, d)
+    c = MoeCfg(experts, top_k, bits, group_size, activation, flags)
+    st = _on(dev, stream, lambda s: lib().gptq_moe_layer(
+        _ptr(X), _DTYPES[dt], tokens, d, f, ctypes.byref(c), _ptr(router), ctypes.byref(u),
+        None if g is None else ctypes.byref(g), ctypes.byref(w), _ptr(topk_ids), _ptr(topk_weights), _ptr(Y),
+        _DTYPES[Y.dtype], _ptr(status), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+    _check(st, "gptq_moe_layer")
 
 
 def gptq_tensor_core_phases(m: int, d: int, n_tokens: int, x_dtype, bits: int, group_size: int = 0,

@@ -264,6 +264,54 @@ gptq_status gptq_fp8_matmul(const void* A, const float* a_scales, const void* B,
                                  static_cast<cudaStream_t>(stream));
 }
 
+size_t gptq_moe_workspace_size(int64_t tokens, int64_t d, int64_t f, int64_t n_experts, int64_t top_k) {
+  if (tokens <= 0 || tokens > 64 || d <= 0 || f <= 0 || d > kMaxDim || f > kMaxDim || d % 32 || f % 32) return 0;
+  if (n_experts <= 0 || n_experts > 256 || top_k <= 0 || top_k > 16) return 0;
+  return gptq::moe_workspace(tokens, d, f, n_experts, top_k);
+}
+
+gptq_status gptq_moe_layer(const void* X, int32_t x_dtype, int64_t tokens, int64_t d, int64_t f,
+                           const gptq_moe_cfg* cfg, const void* router, const gptq_moe_weights* up,
+                           const gptq_moe_weights* gate, const gptq_moe_weights* down, int32_t* topk_ids,
+                           float* topk_weights, void* Y, int32_t y_dtype, int32_t* dev_status, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (cfg == nullptr || up == nullptr || down == nullptr) return GPTQ_ERR_ARG;
+  if (tokens < 0 || tokens > 64 || d <= 0 || f <= 0 || d > kMaxDim || f > kMaxDim || d % 32 || f % 32)
+    return GPTQ_ERR_ARG;
+  if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return GPTQ_ERR_ARG;
+  if (cfg->n_experts <= 0 || cfg->n_experts > 256 || cfg->top_k <= 0 || cfg->top_k > 16) return GPTQ_ERR_ARG;
+  if (router != nullptr && cfg->top_k > cfg->n_experts) return GPTQ_ERR_ARG;
+  if (cfg->bits < 2 || cfg->bits > 4 || (cfg->flags & ~GPTQ_MOE_RENORMALIZE)) return GPTQ_ERR_ARG;
+  if (cfg->activation != GPTQ_ACT_SILU_GATED && cfg->activation != GPTQ_ACT_RELU) return GPTQ_ERR_ARG;
+  const int g = cfg->group_size;
+  if (g < 0 || (g && (g % 32 || d % g || f % g))) return GPTQ_ERR_ARG;
+  const bool gated = cfg->activation == GPTQ_ACT_SILU_GATED;
+  auto given = [](const gptq_moe_weights* w) {
+    return w->packed && w->scales && w->zeros && aligned(w->packed, 16) && aligned(w->scales, 4) &&
+           aligned(w->zeros, 4);
+  };
+  if (!gated && gate != nullptr && (gate->packed || gate->scales || gate->zeros)) return GPTQ_ERR_ARG;
+  if (tokens == 0) return GPTQ_OK;
+  if (!given(up) || !given(down) || (gated && (gate == nullptr || !given(gate)))) return GPTQ_ERR_ARG;
+  if (!X || !topk_ids || !topk_weights || !Y || !dev_status) return GPTQ_ERR_ARG;
+  if (!aligned(X, 16) || !aligned(router, 16) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(Y, dtype_size(y_dtype)) || !aligned(dev_status, 4))
+    return GPTQ_ERR_ARG;
+  const size_t need = gptq::moe_workspace(tokens, d, f, cfg->n_experts, cfg->top_k);
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)) return GPTQ_ERR_WORKSPACE;
+  gptq::MoeArgs m = {};
+  m.X = X, m.x_dtype = x_dtype, m.y_dtype = y_dtype;
+  m.tokens = tokens, m.d = d, m.f = f;
+  m.experts = cfg->n_experts, m.top_k = cfg->top_k, m.group_size = g;
+  m.gated = gated, m.renormalize = (cfg->flags & GPTQ_MOE_RENORMALIZE) != 0;
+  m.router = router;
+  m.up = *up, m.down = *down;
+  if (gated) m.gate = *gate;
+  m.ids = topk_ids, m.weights = topk_weights, m.Y = Y;
+  m.status = dev_status, m.workspace = workspace;
+  return gptq::moe_launch(m, cfg->bits, static_cast<cudaStream_t>(stream));
+}
+
 gptq_status gptq_read_status(const int32_t* dev_status, void* stream, int64_t* detail) {
   if (dev_status == nullptr) return GPTQ_ERR_ARG;
   int32_t h[2] = {0, 0};

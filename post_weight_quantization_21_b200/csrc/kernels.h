@@ -127,6 +127,25 @@ gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* 
                               int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* Y, int32_t y_dtype,
                               int32_t* status, void* workspace, cudaStream_t stream);
 
+// mixture-of-experts layer over packed weights (moe.cu)
+using MoePacked = gptq_moe_weights;
+struct MoeArgs {
+  const void* X;
+  int32_t x_dtype, y_dtype;
+  int64_t tokens, d, f;
+  int experts, top_k, group_size;
+  bool gated, renormalize;
+  const void* router;
+  MoePacked up, gate, down;
+  int32_t* ids;
+  float* weights;
+  void* Y;
+  int32_t* status;
+  void* workspace;
+};
+size_t moe_workspace(int64_t tokens, int64_t d, int64_t f, int64_t experts, int64_t top_k);
+gptq_status moe_launch(const MoeArgs& m, int32_t bits, cudaStream_t stream);
+
 // A7
 gptq_status pack_launch(const uint8_t* codes, int64_t m, int64_t d, int32_t bits, int32_t* packed,
                         cudaStream_t stream);
