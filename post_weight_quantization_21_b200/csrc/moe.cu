@@ -5,22 +5,22 @@
 // with every matrix What[r, j] = scale[r, g] (q[r, j] - zero[r, g]) read as packed codes.
 //
 // The bytes of the chosen experts' codes are the floor, so the work to keep below HBM's time is taking the
-// codes apart.  A code is masked together with the exponent of 128 into a bf16 mantissa: 128 + q 2^p is
-// exact there for q 2^p < 128, and so is the difference with 128 + zero 2^p, (q - zero) 2^p.  Two codes
-// per register, one mask and one subtraction per pair, and the pair is a ready fragment of
-// mma.m16n8k16 (weights on the M side, up to 8 tokens on the N side): a product of M = 8 tokens is no
-// tcgen05 shape, and the tensor pipe has time to spare here.  The order of the columns in a sum is free,
-// so the pairs are the codes that lie 16 bits apart (see Pairs) and the tokens' values are laid out to
-// match, multiplied by 2^-p.
+// codes apart.  A code masked in place into the low bits of an fp16 is a subnormal, q 2^(p - 24) exactly:
+// one AND for two codes, nothing to subtract, and the pair is a ready fragment of mma.m16n8k16 (weights on
+// the M side, up to 8 tokens on the N side: a product with so few columns is no tcgen05 shape, and the tensor
+// pipe has time to spare here).  The order of the columns in a sum is free, so a pair is two codes that lie
+// 16 bits apart (see Pairs) and the tokens' values are laid out to match, multiplied by 2^-p.  The zero point
+// leaves the sum as zero * sum_j x_j, which starts the accumulator: sum_j (q_j - zero) x_j = sum q x - zero sum x.
 //
-// Tokens are split into bf16 terms that add up to the value exactly: one for bf16, two for fp16, three for
-// fp32; the intermediate a_i, kept in fp32, into three, or two when the result has 16 bits (an error of
-// 2^-17 beside the result's own 2^-9 or 2^-12).  Every product is then exact in the tensor core, sums
-// run there over 128 columns (truncated at 2^-24 or so of the partial sum) and in fp32 beyond.
+// Tokens become fp16 terms of x 2^-e, e per token and 128 columns so that the largest value lies below 2^15: one
+// term holds a bf16 or fp16 value exactly as long as it is not below 2^-21 of the block's largest (then it is off
+// by less than 2^-32 of that), two terms hold an fp32 value to 2^-24 of itself.  The intermediate a_i, kept in fp32,
+// takes two terms, or one where Y is bf16 (2^-12 beside the result's own 2^-9).  Products are then exact in
+// the tensor core, sums run there over 128 columns and in fp32 beyond.
 //
 // Launches: router logits and the tokens' layout; top-K and the lists of tokens per expert; the up product
-// with the activation; the down product; the weighted sum in the order of the choice.  No atomics: results
-// are deterministic.
+// with the activation; the activations' layout; the down product; the weighted sum in the order of the choice.
+// No atomics: results are deterministic.
 #include <algorithm>
 
 #include "kernels.h"
@@ -35,128 +35,85 @@ constexpr int kMaxTokens = 64;
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
 
 // ------------------------------------------------------------------ columns of a unit of 32 codes
-// pair(i) = (column in the low half, column in the high half) of the i-th register of a unit, both masked at
-// bit p(i) of their half; the inverse gives a column's register and half.
+// Register i of a unit holds columns lo(i) and hi(i) in its halves, both at bit p(i).
 template <int BITS>
 struct Pairs;
 template <>
-struct Pairs<4> {  // register 4 w + s: word w shifted by 4 s
+struct Pairs<4> {  // register 4 w + 2 h + s: word w shifted by 8 h, masked at bit 4 s
   __host__ __device__ static constexpr int lo(int i) { return 8 * (i / 4) + i % 4; }
   __host__ __device__ static constexpr int hi(int i) { return lo(i) + 4; }
-  __host__ __device__ static constexpr int p(int) { return 0; }
-  __host__ __device__ static constexpr int reg(int j) { return 4 * (j / 8) + j % 4; }
-  __host__ __device__ static constexpr int half(int j) { return j % 8 / 4; }
+  __host__ __device__ static constexpr int p(int i) { return 4 * (i & 1); }
 };
 template <>
-struct Pairs<2> {  // register 8 w + s: word w shifted by 6 (s / 3), three codes of a half per shift
+struct Pairs<2> {  // register 8 w + s: word w, shifted by 10 from s = 5 on
   __host__ __device__ static constexpr int lo(int i) { return 16 * (i / 8) + i % 8; }
   __host__ __device__ static constexpr int hi(int i) { return lo(i) + 8; }
-  __host__ __device__ static constexpr int p(int i) { return 2 * (i % 8 % 3); }
-  __host__ __device__ static constexpr int reg(int j) { return 8 * (j / 16) + j % 8; }
-  __host__ __device__ static constexpr int half(int j) { return j % 16 / 8; }
+  __host__ __device__ static constexpr int p(int i) { return 2 * (i % 8 % 5); }
 };
 template <>
-struct Pairs<3> {  // registers 5 b + s: runs of five codes side by side; register 15: the two codes across words
-  __host__ __device__ static constexpr int lo(int i) { return i == 15 ? 10 : (i < 5 ? i : (i < 10 ? i : i + 12)); }
+struct Pairs<3> {  // registers 5 b + s: two runs of five codes side by side; register 15: the codes across words
+  __host__ __device__ static constexpr int lo(int i) { return i == 15 ? 10 : (i < 10 ? i : i + 12); }
   __host__ __device__ static constexpr int hi(int i) { return i == 15 ? 21 : (i < 10 ? i + 11 : i + 17); }
-  __host__ __device__ static constexpr int p(int i) { return i == 15 ? 0 : 3 * (i % 5 & 1); }
-  __host__ __device__ static constexpr int reg(int j) {
-    return j == 10 || j == 21 ? 15 : (j < 10 ? j : (j < 21 ? j - 11 : 10 + (j - 22) % 5));
-  }
-  __host__ __device__ static constexpr int half(int j) { return j < 11 ? 0 : (j < 22 ? 1 : (j - 22) / 5); }
+  __host__ __device__ static constexpr int p(int i) { return i == 15 ? 0 : 3 * (i % 5 % 3); }
 };
 template <int BITS>
 __host__ __device__ constexpr bool pairs_ok() {
+  uint32_t seen = 0;
   for (int i = 0; i < 16; ++i) {
-    const int l = Pairs<BITS>::lo(i), h = Pairs<BITS>::hi(i);
-    if (Pairs<BITS>::reg(l) != i || Pairs<BITS>::half(l) != 0) return false;
-    if (Pairs<BITS>::reg(h) != i || Pairs<BITS>::half(h) != 1) return false;
-    if ((((1 << BITS) - 1) << Pairs<BITS>::p(i)) >= 128) return false;
+    seen |= 1u << Pairs<BITS>::lo(i) | 1u << Pairs<BITS>::hi(i);
+    if (Pairs<BITS>::p(i) + BITS > 10) return false;  // a subnormal's mantissa
   }
-  return true;
+  return seen == 0xffffffffu;  // every column once
 }
 static_assert(pairs_ok<2>() && pairs_ok<3>() && pairs_ok<4>(), "column order");
 
-constexpr uint32_t kMagic = 0x43004300u;  // 128 in both halves
-
-// (v & (mask << p)) | magic for both halves
 template <int BITS, int P>
 __device__ __forceinline__ uint32_t mask_pair(uint32_t v) {
   constexpr uint32_t m = ((1u << BITS) - 1u) << P;
-  return (v & (m | (m << 16))) | kMagic;
+  return v & (m | (m << 16));
 }
 
-// the 16 registers (128 + q 2^p) of a unit
+// registers 4 q .. 4 q + 3 of a unit: codes q 2^(p - 24) in both halves (q a constant once unrolled)
 template <int BITS>
-__device__ __forceinline__ void unit_pairs(const uint32_t (&w)[BITS], uint32_t (&v)[16]);
+__device__ __forceinline__ void unit_quad(const uint32_t (&w)[BITS], int q, uint32_t (&v)[4]);
 template <>
-__device__ __forceinline__ void unit_pairs<4>(const uint32_t (&w)[4], uint32_t (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = mask_pair<4, 0>(w[i / 4] >> (4 * (i % 4)));
+__device__ __forceinline__ void unit_quad<4>(const uint32_t (&w)[4], int q, uint32_t (&v)[4]) {
+  const uint32_t b = w[q] >> 8;
+  v[0] = mask_pair<4, 0>(w[q]), v[1] = mask_pair<4, 4>(w[q]), v[2] = mask_pair<4, 0>(b), v[3] = mask_pair<4, 4>(b);
 }
 template <>
-__device__ __forceinline__ void unit_pairs<2>(const uint32_t (&w)[2], uint32_t (&v)[16]) {
+__device__ __forceinline__ void unit_quad<2>(const uint32_t (&w)[2], int q, uint32_t (&v)[4]) {
+  const uint32_t a = w[q >> 1], b = w[q >> 1] >> 10;
+  if (q & 1)
+    v[0] = mask_pair<2, 8>(a), v[1] = mask_pair<2, 0>(b), v[2] = mask_pair<2, 2>(b), v[3] = mask_pair<2, 4>(b);
+  else
+    v[0] = mask_pair<2, 0>(a), v[1] = mask_pair<2, 2>(a), v[2] = mask_pair<2, 4>(a), v[3] = mask_pair<2, 6>(a);
+}
+template <>
+__device__ __forceinline__ void unit_quad<3>(const uint32_t (&w)[3], int q, uint32_t (&v)[4]) {
+  // words 0, 1, 2 hold codes 0-9, 11-20 and 22-31 whole, from bits 0, 1 and 2: runs of five, two to a register
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t a = w[k], b = w[k] >> 6, c = w[k] >> 12;
-    v[8 * k + 0] = mask_pair<2, 0>(a), v[8 * k + 1] = mask_pair<2, 2>(a), v[8 * k + 2] = mask_pair<2, 4>(a);
-    v[8 * k + 3] = mask_pair<2, 0>(b), v[8 * k + 4] = mask_pair<2, 2>(b), v[8 * k + 5] = mask_pair<2, 4>(b);
-    v[8 * k + 6] = mask_pair<2, 0>(c), v[8 * k + 7] = mask_pair<2, 2>(c);
+  for (int j = 0; j < 4; ++j) {
+    const int i = 4 * q + j;
+    if (i == 15) {
+      v[j] = mask_pair<3, 0>(__byte_perm(__funnelshift_r(w[0], w[1], 30), __funnelshift_r(w[1], w[2], 31), 0x5410));
+    } else {
+      const uint32_t b = w[1] >> 1, c = w[2] >> 2;
+      const uint32_t run = i < 5 ? __byte_perm(w[0], b, 0x5410)
+                                 : (i < 10 ? __byte_perm(w[0] >> 15, b >> 15, 0x5410) : __byte_perm(c, c >> 15, 0x5410));
+      const int s = i % 5;
+      const uint32_t r = s < 3 ? run : run >> 9;
+      v[j] = s % 3 == 0 ? mask_pair<3, 0>(r) : (s % 3 == 1 ? mask_pair<3, 3>(r) : mask_pair<3, 6>(r));
+    }
   }
 }
-template <>
-__device__ __forceinline__ void unit_pairs<3>(const uint32_t (&w)[3], uint32_t (&v)[16]) {
-  // words 0, 1, 2 hold codes 0-9, 11-20 and 22-31 whole, from bits 0, 1 and 2
-  const uint32_t b = w[1] >> 1, c = w[2] >> 2;
-  const uint32_t run[3] = {__byte_perm(w[0], b, 0x5410), __byte_perm(w[0] >> 15, b >> 15, 0x5410),
-                           __byte_perm(c, c >> 15, 0x5410)};
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const uint32_t s6 = run[k] >> 6, s12 = run[k] >> 12;
-    v[5 * k + 0] = mask_pair<3, 0>(run[k]), v[5 * k + 1] = mask_pair<3, 3>(run[k]);
-    v[5 * k + 2] = mask_pair<3, 0>(s6), v[5 * k + 3] = mask_pair<3, 3>(s6);
-    v[5 * k + 4] = mask_pair<3, 0>(s12);
-  }
-  v[15] = mask_pair<3, 0>(
-      __byte_perm(__funnelshift_r(w[0], w[1], 30), __funnelshift_r(w[1], w[2], 31), 0x5410));
-}
 
-// 128 + zero 2^p in both halves (zero 2^p < 128 for zeros of the grid; others only use their low bits)
-template <int BITS>
-__device__ __forceinline__ uint32_t zero_pair(int32_t z, int p) {
-  const uint32_t h = 0x4300u | (((uint32_t)z << p) & 0x7Fu);
-  return h | (h << 16);
-}
-
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// ------------------------------------------------------------------ bf16 terms
-// v as the sum of `terms` bf16 values, each the nearest to what the ones before leave; a value that is not
-// finite is its own first term.
-template <int TERMS>
-__device__ __forceinline__ void split_bf16(float v, uint16_t (&t)[TERMS]) {
-  const bool finite = (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
-#pragma unroll
-  for (int i = 0; i < TERMS; ++i) {
-    __nv_bfloat16 h = __float2bfloat16_rn(v);
-    // the largest fp32 values round up to infinity: take the largest bf16 and leave the rest to the next term
-    if (finite && (__bfloat16_as_ushort(h) & 0x7FFFu) == 0x7F80u && TERMS > 1)
-      h = __ushort_as_bfloat16((__bfloat16_as_ushort(h) & 0x8000u) | 0x7F7Fu);
-    t[i] = __bfloat16_as_ushort(h);
-    v = finite ? v - __bfloat162float(h) : 0.0f;
-  }
 }
 
 // ------------------------------------------------------------------ workspace
@@ -170,14 +127,25 @@ struct Lists {
   int32_t pairs[kMaxPairs];  // pair = token * top_k + place in the token's choice, grouped by expert
 };
 
-struct Layout {
-  size_t lists, logits, x_terms, a_terms, products, total;
-  int chunks_d, chunks_f;  // 128-column chunks of a token's and of an intermediate row
+// fp16 terms of rows of columns, in the order of Pairs
+struct Terms {
+  uint16_t* values;   // [term][row][chunk][unit of the chunk][register]
+  float2* chunk;      // [row][chunk]: 2^e, sum of x 2^(-e - 24) over the chunk
+  float* unit;        // [row][unit of every chunk]: the same sum over the unit
+  int64_t stride;     // values per term
+  int chunks;         // 128-column chunks per row
 };
-Layout layout_of(int64_t tokens, int64_t d, int64_t f, int64_t experts, int64_t top_k) {
+
+struct Layout {
+  size_t lists, logits, x_terms, a_terms, acts, products, total;
+};
+int chunks_of(int64_t cols) { return (int)((cols + 127) / 128); }
+size_t terms_bytes(int64_t rows, int64_t cols) {
+  return (size_t)rows * chunks_of(cols) * (2 * 256 + sizeof(float2) + 4 * sizeof(float));
+}
+Layout layout_of(int64_t tokens, int64_t d, int64_t f, int64_t top_k, int64_t experts) {
   Layout l;
   const size_t pairs = (size_t)tokens * top_k;
-  l.chunks_d = (int)((d + 127) / 128), l.chunks_f = (int)((f + 127) / 128);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -186,11 +154,21 @@ Layout layout_of(int64_t tokens, int64_t d, int64_t f, int64_t experts, int64_t 
   };
   l.lists = take(sizeof(Lists));
   l.logits = take((size_t)tokens * experts * 4);
-  l.x_terms = take((size_t)3 * tokens * l.chunks_d * 256);
-  l.a_terms = take((size_t)3 * pairs * l.chunks_f * 256);
+  l.x_terms = take(terms_bytes(tokens, d));
+  l.a_terms = take(terms_bytes(pairs, f));
+  l.acts = take(pairs * f * 4);
   l.products = take(pairs * d * 4);
   l.total = at;
   return l;
+}
+Terms terms_at(void* base, int64_t rows, int64_t cols) {
+  Terms t;
+  t.chunks = chunks_of(cols);
+  t.stride = rows * t.chunks * 128;
+  t.values = static_cast<uint16_t*>(base);
+  t.chunk = reinterpret_cast<float2*>(t.values + 2 * t.stride);
+  t.unit = reinterpret_cast<float*>(t.chunk + rows * t.chunks);
+  return t;
 }
 
 // ------------------------------------------------------------------ router logits, tokens' layout
@@ -210,14 +188,73 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
   }
 }
 
+// The terms of one row's unit u of 32 columns (zeros past the last unit); the four lanes of a chunk call it
+// together.
+template <typename T, int BITS, int TERMS>
+__device__ __forceinline__ void layout_unit(const T* __restrict__ row, int64_t r, int u, int units, const Terms& out) {
+  float v[32];
+  float big = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (u < units) load8<T>(row + u * 32 + 8 * q, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[8 * q + k] = x[k];
+      const float m = fabsf(x[k]);
+      big = fmaxf(big, m < INFINITY ? m : 0.0f);
+    }
+  }
+  big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+  // 2^(e + 14) <= big < 2^(e + 15)
+  const int e = big > 0.0f ? max((int)(__float_as_uint(big) >> 23) - 127 - 14, -126) : 0;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  float sum = 0.0f;
+  uint32_t out_v[TERMS][16];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] *= down;  // exact
+    sum += v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float scale = 1.0f / (float)(1 << Pairs<BITS>::p(i));
+    float x[2] = {v[Pairs<BITS>::lo(i)] * scale, v[Pairs<BITS>::hi(i)] * scale};
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const __half t = __float2half_rn(x[h]);
+        word |= (uint32_t)__half_as_ushort(t) << (16 * h);
+        x[h] = fabsf(x[h]) < INFINITY ? x[h] - __half2float(t) : 0.0f;
+      }
+      out_v[k][i] = word;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < TERMS; ++k) {
+    uint4* dst = reinterpret_cast<uint4*>(out.values + k * out.stride + (r * out.chunks * 4 + u) * 32);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      dst[q] = make_uint4(out_v[k][4 * q], out_v[k][4 * q + 1], out_v[k][4 * q + 2], out_v[k][4 * q + 3]);
+  }
+  constexpr float kCode = 1.0f / 16777216.0f;  // 2^-24, a code's unit
+  out.unit[r * out.chunks * 4 + u] = sum * kCode;
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  if ((u & 3) == 0) out.chunk[r * out.chunks + (u >> 2)] = make_float2(__uint_as_float((uint32_t)(e + 127) << 23), sum * kCode);
+}
+
 constexpr int kRouterTokens = 8;  // tokens per CTA of the logits
 
-// CTAs [0, experts * token groups): logits of one expert for up to 8 tokens.  The others: the tokens' terms in
-// the order of Pairs, [term][token][unit][register], a thread per unit of 32 columns.
+// CTAs [0, experts * token groups): logits of one expert for up to 8 tokens.  The others: the tokens' layout, a
+// thread per unit of 32 columns.
 template <typename T, int BITS, int TERMS>
 __global__ void __launch_bounds__(256) moe_router_kernel(const T* __restrict__ X, const T* __restrict__ R, int tokens,
-                                                         int d, int experts, int router_blocks, int chunks,
-                                                         float* __restrict__ logits, uint16_t* __restrict__ terms) {
+                                                         int d, int experts, int router_blocks,
+                                                         float* __restrict__ logits, const Terms terms) {
   if ((int)blockIdx.x < router_blocks) {
     const int e = blockIdx.x % experts, t0 = blockIdx.x / experts * kRouterTokens;
     const int nt = min(kRouterTokens, tokens - t0);
@@ -252,35 +289,24 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const T* __restrict__ X
     }
     return;
   }
-  const int units = d >> 5;
+  const int per_row = terms.chunks * 4;
+  const int64_t n = (int64_t)tokens * per_row;
   const int64_t i = (int64_t)(blockIdx.x - router_blocks) * 256 + threadIdx.x;
-  if (i >= (int64_t)tokens * units) return;
-  const int t = (int)(i / units), u = (int)(i % units);
-  float v[32];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float x[8];
-    load8<T>(X + (int64_t)t * d + u * 32 + 8 * q, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[8 * q + k] = x[k];
-  }
-  uint32_t out[TERMS][16];
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const float scale = 1.0f / (float)(1 << Pairs<BITS>::p(r));
-    uint16_t lo[TERMS], hi[TERMS];
-    split_bf16<TERMS>(v[Pairs<BITS>::lo(r)] * scale, lo);
-    split_bf16<TERMS>(v[Pairs<BITS>::hi(r)] * scale, hi);
-#pragma unroll
-    for (int k = 0; k < TERMS; ++k) out[k][r] = lo[k] | ((uint32_t)hi[k] << 16);
-  }
-#pragma unroll
-  for (int k = 0; k < TERMS; ++k) {
-    uint4* dst = reinterpret_cast<uint4*>(terms + ((int64_t)(k * tokens + t) * chunks * 4 + u) * 32);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      dst[q] = make_uint4(out[k][4 * q], out[k][4 * q + 1], out[k][4 * q + 2], out[k][4 * q + 3]);
-  }
+  const int64_t r = min(i, n - 1) / per_row;  // past the end: the last chunk once more (whole warps shuffle)
+  const int u = (int)(i < n ? i - r * per_row : per_row - 4 + (i & 3));
+  layout_unit<T, BITS, TERMS>(X + r * d, r, u, d >> 5, terms);
+}
+
+// the activations' layout
+template <int BITS, int TERMS>
+__global__ void __launch_bounds__(256) moe_layout_kernel(const float* __restrict__ acts, int64_t rows, int cols,
+                                                         const Terms terms) {
+  const int per_row = terms.chunks * 4;
+  const int64_t n = rows * per_row;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = min(i, n - 1) / per_row;
+  const int u = (int)(i < n ? i - r * per_row : per_row - 4 + (i & 3));
+  layout_unit<float, BITS, TERMS>(acts + r * cols, r, u, cols >> 5, terms);
 }
 
 // ------------------------------------------------------------------ top-K and the lists
@@ -403,15 +429,13 @@ struct ProductArgs {
   Matrix a, b;             // gated: gate and up; else a is the matrix
   int mode, rows, units;   // rows per expert, units of 32 columns per row
   int ng, group_units;     // grids per row, units per grid
-  int chunks, row_tiles;   // 128-column chunks, work items per tile
+  int chunks;              // 128-column chunks
+  int row_tiles;           // 32-row (gated: 16-row) tiles of an expert
+  int k_warps;             // warps that share a row tile's chunks: 1, 2, 4 or 8
   int top_k;
-  const uint16_t* terms;   // [term][row][chunk][unit][register]
-  int64_t term_stride;
+  Terms terms;             // rows: tokens (up) or pairs (down)
   const Lists* lists;
-  uint16_t* out_terms;     // up: terms of the activations [term][pair][...]
-  int64_t out_term_stride;
-  int out_chunks, out_count;
-  float* products;         // down: [pair][rows]
+  float* out;              // [pair][rows]: activations (up) or products (down)
 };
 
 // BITS words of a unit
@@ -434,45 +458,77 @@ __device__ __forceinline__ void load_unit(const uint32_t* p, bool ok, uint32_t (
 
 constexpr int kProductWarps = 8;
 
-// A work item is 32 weight rows (two M tiles of 16: consecutive rows, or the same 16 rows of gate and up) of
-// one expert times up to 8 NT of its tokens.  The CTA's warps take the 128-column chunks in turn; in a
-// chunk the four lanes of a row take a unit of 32 codes each, all in registers, and the next chunk's words
-// are loaded while one is worked on.  After each chunk the sums over 128 columns are scaled into fp32 sums;
-// at the end the warps' sums are added in order through shared memory.
+// A row tile is 32 weight rows as two M tiles of 16 (consecutive rows, or the same 16 rows of gate and up) of one
+// expert, times up to 8 NT of its tokens.  k_warps of the CTA's 8 warps share a row tile's chunks in turn,
+// the others take the next row tiles.  In a chunk the four lanes of a row take a unit of 32 codes each, all in
+// registers; the next chunk's words and grids (the next work item's at an item's end) are loaded while one is
+// worked on.  After each chunk the sums over its 128 columns are scaled into fp32 sums; at the end the
+// warps' sums are added in order through shared memory.
 // SUB: scales change inside a chunk (groups of 32 or 64); each quarter then has accumulators of its own and
 // sees the other quarters' tokens as zeros.
 template <int BITS, int TERMS, int NT, int SUB>
 __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(const ProductArgs a) {
   __shared__ float sums[kProductWarps][32][8 * NT + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int n_items = a.lists->n_tiles * a.row_tiles;
-  const int64_t row_words = (int64_t)a.units * BITS;
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const Tile tile = a.lists->tiles[item / a.row_tiles];
-    const int rt = item % a.row_tiles;
-    // this lane's four rows: g and g + 8 of both M tiles
-    const uint32_t* words[4];
-    const float* scales[4];
-    const int32_t* zeros[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool second = i >= 2;
-      const Matrix& m = a.mode == kUpGated && second ? a.b : a.a;
-      const int row = a.mode == kUpGated ? rt * 16 + g + 8 * (i & 1) : rt * 32 + g + 8 * i;
-      const int64_t r = (int64_t)tile.expert * a.rows + row;
-      words[i] = m.words + r * row_words;
-      scales[i] = m.scales + r * a.ng;
-      zeros[i] = m.zeros + r * a.ng;
-    }
-    // this lane's tokens as a column of B: entry g of every 8
-    const uint16_t* tok[NT];
-    bool here[NT];
+  const int kw = warp & (a.k_warps - 1), rg = warp / a.k_warps;  // place among a row tile's warps; which row tile
+  const int groups = kProductWarps / a.k_warps;
+  const int per_tile = (a.row_tiles + groups - 1) / groups;
+  const int n_items = a.lists->n_tiles * per_tile;
+  const bool gated = a.mode == kUpGated;
+  const uint32_t row_words = (uint32_t)a.units * BITS;
+  const int tile_rows = gated ? 16 : 32;
+
+  // this warp's row tile of an item: the first row of M tile 0, and what M tile 1 adds to it (16 rows, or the
+  // way from gate to up)
+  const uint32_t* words;
+  const float* scales;
+  const int32_t* zeros;
+  const int64_t words1 = gated ? a.b.words - a.a.words : 16 * (int64_t)row_words;
+  const int64_t scales1 = gated ? a.b.scales - a.a.scales : 16 * (int64_t)a.ng;
+  const int64_t zeros1 = gated ? a.b.zeros - a.a.zeros : 16 * (int64_t)a.ng;
+  auto set_rows = [&](int item, int expert) {
+    const int64_t r = (int64_t)expert * a.rows + min(item % per_tile * groups + rg, a.row_tiles - 1) * tile_rows + g;
+    words = a.a.words + r * row_words + t * BITS;
+    scales = a.a.scales + r * a.ng;
+    zeros = a.a.zeros + r * a.ng;
+  };
+  uint32_t next[4][BITS];
+  float next_s[4];    // SUB > 1: of this lane's unit
+  int32_t next_z[4];
+  auto load = [&](int c) {
+    const bool ok = 4 * c + t < a.units;
+    const uint32_t* w = words + (uint32_t)c * (4 * BITS);
+    load_unit<BITS>(w, ok, next[0]);
+    load_unit<BITS>(w + 8 * row_words, ok, next[1]);
+    load_unit<BITS>(w + words1, ok, next[2]);
+    load_unit<BITS>(w + words1 + 8 * row_words, ok, next[3]);
+    const int grid = min(SUB == 1 ? 4 * c : 4 * c + t, a.units - 1) / a.group_units;
+    next_s[0] = __ldg(scales + grid), next_s[1] = __ldg(scales + grid + 8 * a.ng);
+    next_s[2] = __ldg(scales + grid + scales1), next_s[3] = __ldg(scales + grid + scales1 + 8 * a.ng);
+    next_z[0] = __ldg(zeros + grid), next_z[1] = __ldg(zeros + grid + 8 * a.ng);
+    next_z[2] = __ldg(zeros + grid + zeros1), next_z[3] = __ldg(zeros + grid + zeros1 + 8 * a.ng);
+  };
+
+  int item = blockIdx.x;
+  if (item >= n_items) return;
+  set_rows(item, a.lists->tiles[item / per_tile].expert);
+  if (kw < a.chunks) load(kw);
+  for (; item < n_items; item += gridDim.x) {
+    const int first = a.lists->tiles[item / per_tile].first, count = a.lists->tiles[item / per_tile].count;
+    const int next_item = item + gridDim.x;
+    const int next_expert = next_item < n_items ? a.lists->tiles[next_item / per_tile].expert : 0;
+    // entry g of every 8 tokens is this lane's column of B; entries 2 t and 2 t + 1 are its columns of the sums
+    constexpr uint32_t kNone = 0xffffffffu;
+    uint32_t tok[NT], col[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      here[n] = 8 * n + g < tile.count;
-      const int p = here[n] ? a.lists->pairs[tile.first + 8 * n + g] : 0;
-      tok[n] = a.terms + (int64_t)(a.mode == kDown ? p : p / a.top_k) * a.chunks * 128 + t * 32;
+      auto row_at = [&](int i) {
+        const int p = a.lists->pairs[first + min(i, count - 1)];
+        return (uint32_t)(a.mode == kDown ? p : p / a.top_k) * (uint32_t)a.chunks;
+      };
+      tok[n] = 8 * n + g < count ? row_at(8 * n + g) * 128 + t * 32 : kNone;
+      col[n][0] = row_at(8 * n + 2 * t), col[n][1] = row_at(8 * n + 2 * t + 1);
     }
     float acc[2][NT][4];
 #pragma unroll
@@ -481,53 +537,67 @@ __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(cons
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-    uint32_t next[4][BITS];
-    auto load_words = [&](int c) {
-      const int u = 4 * c + t;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) load_unit<BITS>(words[i] + (int64_t)u * BITS, u < a.units, next[i]);
-    };
-    load_words(warp);
-    for (int c = warp; c < a.chunks; c += kProductWarps) {
-      const int u = 4 * c + t;
-      const bool unit_here = u < a.units;
-      const int grid = min(u, a.units - 1) / a.group_units;
-      uint32_t v[4][16];
+    for (int c = kw; c < a.chunks; c += a.k_warps) {
+      uint32_t w[4][BITS];
+      float sc[4], z[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        unit_pairs<BITS>(next[i], v[i]);
-        const int32_t z = __ldg(zeros[i] + grid);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[i][r] = sub_bf16x2(v[i][r], zero_pair<BITS>(z, Pairs<BITS>::p(r)));
+        for (int k = 0; k < BITS; ++k) w[i][k] = next[i][k];
+        sc[i] = next_s[i] * 16777216.0f, z[i] = -(float)next_z[i];
       }
-      load_words(c + kProductWarps);
-      float sum[SUB][2][NT][4];
+      if (c + a.k_warps < a.chunks) {
+        load(c + a.k_warps);
+      } else if (next_item < n_items) {
+        set_rows(next_item, next_expert);
+        load(kw);
+      }
+      const bool unit_here = 4 * c + t < a.units;
+      // lane s of the four holds the scale and the zero of quarter s
+      auto quarter = [&](float v, int s) { return SUB == 1 ? v : __shfl_sync(0xffffffffu, v, (lane & 28) | s); };
+      // the accumulators start at -zero sum x; row g of an M tile is in values 0 and 1, row g + 8 in 2 and 3
+      float sum[NT][SUB][2][4];
 #pragma unroll
-      for (int s = 0; s < SUB; ++s)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[s][m][n][i] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < TERMS; ++k) {
+      for (int s = 0; s < SUB; ++s) {
+        const float zs[4] = {quarter(z[0], s), quarter(z[1], s), quarter(z[2], s), quarter(z[3], s)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (8 * n >= tile.count) break;
-          const uint4* src = reinterpret_cast<const uint4*>(tok[n] + k * a.term_stride + (int64_t)c * 128);
+          if (8 * n >= count) break;
+          float x0, x1;
+          if constexpr (SUB == 1) {
+            x0 = __ldg(&a.terms.chunk[col[n][0] + c].y), x1 = __ldg(&a.terms.chunk[col[n][1] + c].y);
+          } else {
+            x0 = __ldg(a.terms.unit + ((col[n][0] + c) * 4 + s)), x1 = __ldg(a.terms.unit + ((col[n][1] + c) * 4 + s));
+          }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 x = here[n] && unit_here ? __ldg(src + q) : make_uint4(0, 0, 0, 0);
+          for (int m = 0; m < 2; ++m) {
+            sum[n][s][m][0] = zs[2 * m] * x0, sum[n][s][m][1] = zs[2 * m] * x1;
+            sum[n][s][m][2] = zs[2 * m + 1] * x0, sum[n][s][m][3] = zs[2 * m + 1] * x1;
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // registers 4 q .. 4 q + 3 of the units: 32 of the chunk's columns
+        uint32_t v[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unit_quad<BITS>(w[i], q, v[i]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (8 * n >= count) break;
+#pragma unroll
+          for (int k = TERMS - 1; k >= 0; --k) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (tok[n] != kNone && unit_here)
+              x = __ldg(reinterpret_cast<const uint4*>(a.terms.values + k * a.terms.stride + (tok[n] + c * 128)) + q);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
 #pragma unroll
               for (int s = 0; s < SUB; ++s) {
                 const bool mine = SUB == 1 || t == s;
-                mma_bf16(sum[s][m][n], v[2 * m][4 * q], v[2 * m + 1][4 * q], v[2 * m][4 * q + 1], v[2 * m + 1][4 * q + 1],
-                         mine ? x.x : 0u, mine ? x.y : 0u);
-                mma_bf16(sum[s][m][n], v[2 * m][4 * q + 2], v[2 * m + 1][4 * q + 2], v[2 * m][4 * q + 3],
-                         v[2 * m + 1][4 * q + 3], mine ? x.z : 0u, mine ? x.w : 0u);
+                mma_f16(sum[n][s][m], v[2 * m][0], v[2 * m + 1][0], v[2 * m][1], v[2 * m + 1][1], mine ? x.x : 0u,
+                        mine ? x.y : 0u);
+                mma_f16(sum[n][s][m], v[2 * m][2], v[2 * m + 1][2], v[2 * m][3], v[2 * m + 1][3], mine ? x.z : 0u,
+                        mine ? x.w : 0u);
               }
             }
           }
@@ -535,16 +605,17 @@ __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(cons
       }
 #pragma unroll
       for (int s = 0; s < SUB; ++s) {
-        const int sg = SUB == 1 ? 4 * c / a.group_units : min(4 * c + s, a.units - 1) / a.group_units;
+        const float ss[4] = {quarter(sc[0], s), quarter(sc[1], s), quarter(sc[2], s), quarter(sc[3], s)};
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const float s0 = __ldg(scales[2 * m] + sg), s1 = __ldg(scales[2 * m + 1] + sg);
+        for (int n = 0; n < NT; ++n) {
+          if (8 * n >= count) break;
+          const float e0 = __ldg(&a.terms.chunk[col[n][0] + c].x), e1 = __ldg(&a.terms.chunk[col[n][1] + c].x);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[m][n][0] = fmaf(s0, sum[s][m][n][0], acc[m][n][0]);
-            acc[m][n][1] = fmaf(s0, sum[s][m][n][1], acc[m][n][1]);
-            acc[m][n][2] = fmaf(s1, sum[s][m][n][2], acc[m][n][2]);
-            acc[m][n][3] = fmaf(s1, sum[s][m][n][3], acc[m][n][3]);
+          for (int m = 0; m < 2; ++m) {
+            acc[m][n][0] = fmaf(ss[2 * m] * e0, sum[n][s][m][0], acc[m][n][0]);
+            acc[m][n][1] = fmaf(ss[2 * m] * e1, sum[n][s][m][1], acc[m][n][1]);
+            acc[m][n][2] = fmaf(ss[2 * m + 1] * e0, sum[n][s][m][2], acc[m][n][2]);
+            acc[m][n][3] = fmaf(ss[2 * m + 1] * e1, sum[n][s][m][3], acc[m][n][3]);
           }
         }
       }
@@ -559,36 +630,20 @@ __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(cons
         lo[0] = acc[m][n][0], lo[1] = acc[m][n][1], hi[0] = acc[m][n][2], hi[1] = acc[m][n][3];
       }
     __syncthreads();
-    auto total = [&](int r, int n) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kProductWarps; ++w) s += sums[w][r][n];
-      return s;
-    };
-    const int out_rows = a.mode == kUpGated ? 16 : 32;
-    for (int i = threadIdx.x; i < out_rows * tile.count; i += kProductWarps * 32) {
-      const int r = i % out_rows, n = i / out_rows;
-      const int p = a.lists->pairs[tile.first + n];
-      const int row = rt * out_rows + r;
-      if (a.mode == kDown) {
-        a.products[(int64_t)p * a.rows + row] = total(r, n);
-        continue;
+    for (int i = threadIdx.x; i < groups * tile_rows * count; i += kProductWarps * 32) {
+      const int r = i % tile_rows, j = i / tile_rows % groups, n = i / (tile_rows * groups);
+      const int rt = item % per_tile * groups + j;
+      if (rt >= a.row_tiles) continue;
+      float v = 0.0f, up = 0.0f;
+      for (int w = j * a.k_warps; w < (j + 1) * a.k_warps; ++w) {
+        v += sums[w][r][n];
+        if (gated) up += sums[w][16 + r][n];
       }
-      float h;
-      if (a.mode == kUpGated) {
-        const float gate = total(r, n);
-        h = gate / (1.0f + expf(-gate)) * total(16 + r, n);
-      } else {
-        h = total(r, n);
-        h = h < 0.0f ? 0.0f : h;  // NaN stays
-      }
-      // its place among the next product's columns
-      const int j = row & 31;
-      const int reg = Pairs<BITS>::reg(j);
-      uint16_t terms[3];
-      split_bf16<3>(h * (1.0f / (float)(1 << Pairs<BITS>::p(reg))), terms);
-      uint16_t* dst = a.out_terms + ((int64_t)p * a.out_chunks * 4 + (row >> 5)) * 32 + 2 * reg + Pairs<BITS>::half(j);
-      for (int k = 0; k < a.out_count; ++k) dst[k * a.out_term_stride] = terms[k];
+      if (gated)
+        v = v / (1.0f + expf(-v)) * up;
+      else if (a.mode == kUpRelu)
+        v = v < 0.0f ? 0.0f : v;  // NaN stays
+      a.out[(int64_t)a.lists->pairs[first + n] * a.rows + rt * tile_rows + r] = v;
     }
   }
 }
@@ -621,70 +676,76 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const float* __restric
 }
 
 // ------------------------------------------------------------------ launches
+// warps per row tile: the fewest steps of a chunk along the longest chain of work items, an item's own
+// start and end counted as two steps
+int choose_k_warps(const ProductArgs& a, int tiles, int slots) {
+  int best = 8;
+  int64_t best_cost = INT64_MAX;
+  for (int kw = 8; kw >= 1; kw /= 2) {
+    const int groups = kProductWarps / kw;
+    const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
+    const int64_t cost = (items + slots - 1) / slots * ((a.chunks + kw - 1) / kw + 2);
+    if (cost < best_cost) best = kw, best_cost = cost;
+  }
+  return best;
+}
+
 template <int BITS, int TERMS>
-gptq_status launch_product(const ProductArgs& a, int nt, bool sub, int max_tiles, int sms, cudaStream_t s) {
-  const int64_t items = (int64_t)max_tiles * a.row_tiles;
-  const int grid = (int)std::min<int64_t>(items, 2 * (int64_t)sms);
+gptq_status launch_product(ProductArgs a, int nt, bool sub, int tiles, int sms, cudaStream_t s) {
+  const int slots = 2 * sms;
+  a.k_warps = choose_k_warps(a, tiles, slots);
+  const int groups = kProductWarps / a.k_warps;
+  const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
+  const int grid = (int)std::min<int64_t>(items, slots);
   if (sub)
     moe_product_kernel<BITS, TERMS, 1, 4><<<grid, kProductWarps * 32, 0, s>>>(a);
   else if (nt == 1)
     moe_product_kernel<BITS, TERMS, 1, 1><<<grid, kProductWarps * 32, 0, s>>>(a);
   else
-    moe_product_kernel<BITS, TERMS, 4, 1><<<grid, kProductWarps * 32, 0, s>>>(a);
+    moe_product_kernel<BITS, TERMS, 2, 1><<<grid, kProductWarps * 32, 0, s>>>(a);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
-template <int BITS>
-gptq_status launch_product_terms(int terms, const ProductArgs& a, int nt, bool sub, int max_tiles, int sms,
-                                 cudaStream_t s) {
-  switch (terms) {
-    case 1: return launch_product<BITS, 1>(a, nt, sub, max_tiles, sms, s);
-    case 2: return launch_product<BITS, 2>(a, nt, sub, max_tiles, sms, s);
-    default: return launch_product<BITS, 3>(a, nt, sub, max_tiles, sms, s);
-  }
-}
-
 template <typename T, int BITS, int TERMS>
-gptq_status launch_router(const void* X, const void* R, int tokens, int d, int experts, int chunks, float* logits,
-                          uint16_t* terms, cudaStream_t s) {
-  const int router_blocks = R ? experts * ((tokens + kRouterTokens - 1) / kRouterTokens) : 0;
-  const int layout_blocks = (int)(((int64_t)tokens * (d / 32) + 255) / 256);
+gptq_status launch_router(const MoeArgs& m, float* logits, const Terms& terms, cudaStream_t s) {
+  const int tokens = (int)m.tokens, d = (int)m.d;
+  const int router_blocks = m.router ? m.experts * ((tokens + kRouterTokens - 1) / kRouterTokens) : 0;
+  const int layout_blocks = (int)(((int64_t)tokens * terms.chunks * 4 + 255) / 256);
   moe_router_kernel<T, BITS, TERMS><<<router_blocks + layout_blocks, 256, 0, s>>>(
-      static_cast<const T*>(X), static_cast<const T*>(R), tokens, d, experts, router_blocks, chunks, logits, terms);
+      static_cast<const T*>(m.X), static_cast<const T*>(m.router), tokens, d, m.experts, router_blocks, logits, terms);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
 template <int BITS>
 gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
-  const Layout l = layout_of(m.tokens, m.d, m.f, m.experts, m.top_k);
+  const Layout l = layout_of(m.tokens, m.d, m.f, m.top_k, m.experts);
   char* ws = static_cast<char*>(m.workspace);
   Lists* lists = reinterpret_cast<Lists*>(ws + l.lists);
   float* logits = reinterpret_cast<float*>(ws + l.logits);
-  uint16_t* x_terms = reinterpret_cast<uint16_t*>(ws + l.x_terms);
-  uint16_t* a_terms = reinterpret_cast<uint16_t*>(ws + l.a_terms);
+  float* acts = reinterpret_cast<float*>(ws + l.acts);
   float* products = reinterpret_cast<float*>(ws + l.products);
   int dev = 0, sms = 0;
   GPTQ_CUDA_TRY(cudaGetDevice(&dev));
   GPTQ_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const int tokens = (int)m.tokens, d = (int)m.d, f = (int)m.f;
   const int pairs = tokens * m.top_k;
-  const int x_count = m.x_dtype == GPTQ_BF16 ? 1 : (m.x_dtype == GPTQ_FP16 ? 2 : 3);
-  const int a_count = m.y_dtype == GPTQ_FP32 ? 3 : 2;
+  const Terms x_terms = terms_at(ws + l.x_terms, tokens, d), a_terms = terms_at(ws + l.a_terms, pairs, f);
+  const bool x_wide = m.x_dtype == GPTQ_FP32, a_wide = m.y_dtype != GPTQ_BF16;
   gptq_status st;
   switch (m.x_dtype) {
-    case GPTQ_BF16: st = launch_router<__nv_bfloat16, BITS, 1>(m.X, m.router, tokens, d, m.experts, l.chunks_d, logits, x_terms, s); break;
-    case GPTQ_FP16: st = launch_router<__half, BITS, 2>(m.X, m.router, tokens, d, m.experts, l.chunks_d, logits, x_terms, s); break;
-    default: st = launch_router<float, BITS, 3>(m.X, m.router, tokens, d, m.experts, l.chunks_d, logits, x_terms, s); break;
+    case GPTQ_BF16: st = launch_router<__nv_bfloat16, BITS, 1>(m, logits, x_terms, s); break;
+    case GPTQ_FP16: st = launch_router<__half, BITS, 1>(m, logits, x_terms, s); break;
+    default: st = launch_router<float, BITS, 2>(m, logits, x_terms, s); break;
   }
   if (st != GPTQ_OK) return st;
-  // up to 8 tokens an expert's list is one N tile; longer lists go 32 at a time so that the codes are taken
-  // apart once for four N tiles (scales that change inside a chunk need the registers: 8 at a time)
+  // up to 8 tokens an expert's list is one N tile; longer lists go 16 at a time so that the codes are taken
+  // apart once for two N tiles (scales that change inside a chunk need the registers: 8 at a time)
   const bool sub = m.group_size == 32 || m.group_size == 64;
-  const int nt = pairs <= 8 || sub ? 1 : 4;
+  const int nt = tokens <= 8 || sub ? 1 : 2;
   const int tile_tokens = 8 * nt;
-  const int max_tiles = std::min(pairs, std::min(m.experts, pairs) + pairs / tile_tokens);
+  const int tiles = std::min(pairs, std::min(m.experts, pairs) + pairs / tile_tokens);  // at most
   moe_route_kernel<<<1, 1024, 0, s>>>(m.router ? logits : nullptr, tokens, m.experts, m.top_k, m.renormalize,
                                       tile_tokens, m.ids, m.weights, lists, m.status);
   GPTQ_LAUNCH_CHECK();
@@ -698,23 +759,28 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   a.rows = f, a.units = d / 32;
   a.ng = m.group_size ? d / m.group_size : 1;
   a.group_units = m.group_size ? m.group_size / 32 : a.units;
-  a.chunks = l.chunks_d, a.row_tiles = m.gated ? f / 16 : f / 32;
+  a.chunks = x_terms.chunks, a.row_tiles = m.gated ? f / 16 : f / 32;
   a.top_k = m.top_k;
-  a.terms = x_terms, a.term_stride = (int64_t)tokens * l.chunks_d * 128;
+  a.terms = x_terms;
   a.lists = lists;
-  a.out_terms = a_terms, a.out_term_stride = (int64_t)pairs * l.chunks_f * 128;
-  a.out_chunks = l.chunks_f, a.out_count = a_count;
-  st = launch_product_terms<BITS>(x_count, a, nt, sub, max_tiles, sms, s);
+  a.out = acts;
+  st = x_wide ? launch_product<BITS, 2>(a, nt, sub, tiles, sms, s) : launch_product<BITS, 1>(a, nt, sub, tiles, sms, s);
   if (st != GPTQ_OK) return st;
+  const unsigned layout_blocks = (unsigned)(((int64_t)pairs * a_terms.chunks * 4 + 255) / 256);
+  if (a_wide)
+    moe_layout_kernel<BITS, 2><<<layout_blocks, 256, 0, s>>>(acts, pairs, f, a_terms);
+  else
+    moe_layout_kernel<BITS, 1><<<layout_blocks, 256, 0, s>>>(acts, pairs, f, a_terms);
+  GPTQ_LAUNCH_CHECK();
   a.mode = kDown;
   a.a = matrix(m.down);
   a.rows = d, a.units = f / 32;
   a.ng = m.group_size ? f / m.group_size : 1;
   a.group_units = m.group_size ? m.group_size / 32 : a.units;
-  a.chunks = l.chunks_f, a.row_tiles = d / 32;
-  a.terms = a_terms, a.term_stride = (int64_t)pairs * l.chunks_f * 128;
-  a.products = products;
-  st = launch_product_terms<BITS>(a_count, a, nt, sub, max_tiles, sms, s);
+  a.chunks = a_terms.chunks, a.row_tiles = d / 32;
+  a.terms = a_terms;
+  a.out = products;
+  st = a_wide ? launch_product<BITS, 2>(a, nt, sub, tiles, sms, s) : launch_product<BITS, 1>(a, nt, sub, tiles, sms, s);
   if (st != GPTQ_OK) return st;
   const unsigned blocks = (unsigned)(((int64_t)tokens * d + 255) / 256);
   switch (m.y_dtype) {
@@ -729,7 +795,7 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
 }  // namespace
 
 size_t moe_workspace(int64_t tokens, int64_t d, int64_t f, int64_t experts, int64_t top_k) {
-  return layout_of(tokens, d, f, experts, top_k).total;
+  return layout_of(tokens, d, f, top_k, experts).total;
 }
 
 gptq_status moe_launch(const MoeArgs& m, int32_t bits, cudaStream_t stream) {

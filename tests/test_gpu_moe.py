@@ -14,15 +14,15 @@ U = 2.0 ** -24  # fp32 rounding
 
 
 def _experts(e, rows, cols, bits, gs, gen, dev):
-    """((packed, scales, zeros) on the device, What [e, rows, cols] fp64)"""
+    """((packed, scales, zeros) on the device, What and scale * (q + zero) [e, rows, cols] fp64)"""
     codes = torch.randint(0, 2 ** bits, (e, rows, cols), generator=gen)
     ng = cols // gs if gs else 1
     scales = ((torch.rand(e, rows, ng, generator=gen) + 0.5) / (cols ** 0.5 * 2 ** (bits - 2))).float()
     zeros = torch.randint(0, 2 ** bits, (e, rows, ng), generator=gen, dtype=torch.int32)
     packed = oracle.pack_codes(codes.reshape(e * rows, cols).numpy(), bits).reshape(e, rows, -1)
     rep = gs or cols
-    W = scales.double().repeat_interleave(rep, -1) * (codes.double() - zeros.double().repeat_interleave(rep, -1))
-    return (torch.from_numpy(packed).to(dev), scales.to(dev), zeros.to(dev)), W.to(dev)
+    s, q, z = scales.double().repeat_interleave(rep, -1), codes.double(), zeros.double().repeat_interleave(rep, -1)
+    return (torch.from_numpy(packed).to(dev), scales.to(dev), zeros.to(dev)), (s * (q - z)).to(dev), (s * (q + z)).to(dev)
 
 
 class Case:
@@ -32,9 +32,9 @@ class Case:
         self.t, self.e, self.top, self.d, self.f, self.bits, self.gs, self.ydt, self.act = t, e, top, d, f, bits, gs, ydt, act
         self.x = torch.randn(t, d, generator=gen).to(xdt).to(dev)
         self.router = (torch.randn(e, d, generator=gen) * (2.0 / d ** 0.5)).to(xdt).to(dev)
-        self.up, self.Wu = _experts(e, f, d, bits, gs, gen, dev)
-        self.gate, self.Wg = _experts(e, f, d, bits, gs, gen, dev) if act == g.GPTQ_ACT_SILU_GATED else (None, None)
-        self.down, self.Wd = _experts(e, d, f, bits, gs, gen, dev)
+        self.up, self.Wu, self.Au = _experts(e, f, d, bits, gs, gen, dev)
+        self.gate, self.Wg, self.Ag = _experts(e, f, d, bits, gs, gen, dev) if act == g.GPTQ_ACT_SILU_GATED else (None,) * 3
+        self.down, self.Wd, self.Ad = _experts(e, d, f, bits, gs, gen, dev)
         self.ids = torch.full((t, top), -7, dtype=torch.int32, device=dev)
         self.w = torch.full((t, top), float("nan"), device=dev)
         self.Y = torch.full((t, d), float("nan"), device=dev, dtype=ydt)
@@ -69,33 +69,41 @@ class Case:
         assert ((self.w.double() - w).abs() <= tol).all()
 
     def check(self):
-        """Y against fp64 with the device's own choice and weights.  With n sums on a term's way, an fp32 sum is off by at
-        most n u sum|terms|.  Inside a chunk of 128 columns the tensor core adds 128 exact products per bf16 term
-        (at most 3 terms), each addition counted as truncating (2 u); then come the scale, the chunks and
-        8 warps: n = 2 * 3 * 128 + 2 + chunks + 8.  silu's slope is below 1.1 and its own evaluation a few u;
-        the intermediate keeps 24 bits for fp32 results (u) and 16 for 16-bit ones (2^-17), per value."""
-        kb = lambda c: 2 * 3 * 128 + 10 + -(-c // 128)
+        """Y against fp64 with the device's own choice and weights.  A product is formed as s (sum q x - z sum x), so the
+        terms of its sum are s q x and s z x; with n roundings on a term's way the fp32 sum is off by at most n u
+        sum s (q + z) |x|.  n: at most two fp16 terms of x, each 8 tensor-core steps that add 16 exact products, counted
+        as 17 additions that may truncate (2 u each): 544; sum x and its product with z: 36; the scale's product, the
+        chunks of 128 columns and 8 warps: 2 + chunks + 8.  x itself: 2^-24 of each value where it takes two terms
+        (fp32), exact where one holds it, and in both 2^-32 of the block's largest for values too small for fp16.
+        silu's slope is below 1.1 and its own evaluation a few u; the intermediate takes two terms (2^-24 of each value),
+        or one for a bf16 result (2^-12)."""
+
+        def product(W, A, v, ev, own):  # W v with |v's error| <= ev; own: v's rounding to its terms
+            n = 544 + 36 + 10 + -(-v.numel() // 128)
+            ev = ev + own * v.abs() + 2.0 ** -32 * v.abs().max()
+            return W @ v, n * U * (A @ v.abs()) + A @ ev
+
         x, ids, w = self.x.double(), self.ids.long(), self.w.double()
-        wide = self.ydt == torch.float32
+        xown = 2.0 ** -24 if self.x.dtype == torch.float32 else 0.0
+        hown = 2.0 ** -12 if self.ydt == torch.bfloat16 else 2.0 ** -24
         y, tol = torch.zeros_like(x), torch.zeros_like(x)
         for k in range(self.top):
             for t in range(self.t):
                 e = int(ids[t, k])
                 if not 0 <= e < self.e:
                     continue
-                u, eu = self.Wu[e] @ x[t], kb(self.d) * U * (self.Wu[e].abs() @ x[t].abs())
+                u, eu = product(self.Wu[e], self.Au[e], x[t], 0.0, xown)
                 if self.act == g.GPTQ_ACT_SILU_GATED:
-                    z, ez = self.Wg[e] @ x[t], kb(self.d) * U * (self.Wg[e].abs() @ x[t].abs())
+                    z, ez = product(self.Wg[e], self.Ag[e], x[t], 0.0, xown)
                     sl = z * torch.sigmoid(z)
                     h = sl * u
                     eh = 1.1 * ez * (u.abs() + eu) + sl.abs() * eu + 16 * U * h.abs()
                 else:
                     h, eh = torch.relu(u), eu
-                eh = eh + (U if wide else 2.0 ** -17) * h.abs()
-                y[t] += w[t, k] * (self.Wd[e] @ h)
-                mag = self.Wd[e].abs() @ h.abs()
-                tol[t] += w[t, k] * (self.Wd[e].abs() @ eh + (kb(self.f) + 2 + self.top) * U * mag)
-        if not wide:
+                v, ev = product(self.Wd[e], self.Ad[e], h, eh, hown)
+                y[t] += w[t, k] * v
+                tol[t] += w[t, k] * (ev + (2 + self.top) * U * v.abs())
+        if self.ydt != torch.float32:
             tol = tol + torch.finfo(self.ydt).eps / 2 * (y.abs() + tol) + 2.0 ** -25
         assert torch.isfinite(self.Y).all()
         off = (self.Y.double() - y).abs()
@@ -189,6 +197,7 @@ def test_large_values_do_not_overflow_early():
     c.x.mul_(2.0 ** 110)
     c.up[1].mul_(2.0 ** -110)
     c.Wu.mul_(2.0 ** -110)
+    c.Au.mul_(2.0 ** -110)
     c.ids.fill_(1)
     c.w.fill_(0.5)
     c.run(router=False)
