@@ -129,7 +129,7 @@ struct Lists {
 
 // fp16 terms of rows of columns, in the order of Pairs
 struct Terms {
-  uint16_t* values;   // [term][row][chunk][unit of the chunk][register]
+  uint16_t* values;   // [term][row][chunk][quad of registers][unit of the chunk][register of the quad]
   float2* chunk;      // [row][chunk]: 2^e, sum of x 2^(-e - 24) over the chunk
   float* unit;        // [row][unit of every chunk]: the same sum over the unit
   int64_t stride;     // values per term
@@ -166,8 +166,8 @@ Terms terms_at(void* base, int64_t rows, int64_t cols) {
   t.chunks = chunks_of(cols);
   t.stride = rows * t.chunks * 128;
   t.values = static_cast<uint16_t*>(base);
-  t.chunk = reinterpret_cast<float2*>(t.values + 2 * t.stride);
-  t.unit = reinterpret_cast<float*>(t.chunk + rows * t.chunks);
+  t.unit = reinterpret_cast<float*>(t.values + 2 * t.stride);  // a chunk's four start on 16 bytes
+  t.chunk = reinterpret_cast<float2*>(t.unit + 4 * rows * t.chunks);
   return t;
 }
 
@@ -235,10 +235,10 @@ __device__ __forceinline__ void layout_unit(const T* __restrict__ row, int64_t r
   }
 #pragma unroll
   for (int k = 0; k < TERMS; ++k) {
-    uint4* dst = reinterpret_cast<uint4*>(out.values + k * out.stride + (r * out.chunks * 4 + u) * 32);
+    uint4* dst = reinterpret_cast<uint4*>(out.values + k * out.stride + (r * out.chunks + (u >> 2)) * 128) + (u & 3);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      dst[q] = make_uint4(out_v[k][4 * q], out_v[k][4 * q + 1], out_v[k][4 * q + 2], out_v[k][4 * q + 3]);
+      dst[4 * q] = make_uint4(out_v[k][4 * q], out_v[k][4 * q + 1], out_v[k][4 * q + 2], out_v[k][4 * q + 3]);
   }
   constexpr float kCode = 1.0f / 16777216.0f;  // 2^-24, a code's unit
   out.unit[r * out.chunks * 4 + u] = sum * kCode;
@@ -429,106 +429,203 @@ struct ProductArgs {
   Matrix a, b;             // gated: gate and up; else a is the matrix
   int mode, rows, units;   // rows per expert, units of 32 columns per row
   int ng, group_units;     // grids per row, units per grid
+  uint32_t grid_magic;     // ceil(2^32 / group_units): u / group_units in the high word, exact for u < 2^16
   int chunks;              // 128-column chunks
   int row_tiles;           // 32-row (gated: 16-row) tiles of an expert
   int k_warps;             // warps that share a row tile's chunks: 1, 2, 4 or 8
-  int top_k;
+  int cols;                // tokens of a tile at most
+  int top_k, pairs;
   Terms terms;             // rows: tokens (up) or pairs (down)
   const Lists* lists;
   float* out;              // [pair][rows]: activations (up) or products (down)
 };
 
-// BITS words of a unit
-template <int BITS>
-__device__ __forceinline__ void load_unit(const uint32_t* p, bool ok, uint32_t (&w)[BITS]) {
-#pragma unroll
-  for (int i = 0; i < BITS; ++i) w[i] = 0;
-  if (!ok) return;
-  if constexpr (BITS == 4) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else if constexpr (BITS == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = v.x, w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < BITS; ++i) w[i] = __ldg(p + i);
-  }
+constexpr int kProductWarps = 8;
+constexpr int kStages = 3;
+constexpr float kCodeInverse = 16777216.0f;  // 2^24
+
+// CTAs on an SM: registers (80 or 128 a thread) and shared memory are held to it
+template <int NT, int SUB>
+__host__ __device__ constexpr int ctas_per_sm() {
+  return NT == 1 && SUB == 1 ? 3 : 2;
 }
 
-constexpr int kProductWarps = 8;
+// shared memory of one stage: every warp's codes and grids, every group's tokens (see moe_product_kernel)
+template <int BITS, int SUB>
+__host__ __device__ constexpr int warp_stage_bytes() {
+  return 512 * BITS + 2 * 32 * SUB * 4;
+}
+__host__ __device__ inline int token_stage_bytes(int cols, int terms, int sub) {
+  return cols * (terms * 256 + 16 + (sub > 1 ? 16 : 0));
+}
+
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok = true) {  // zeros where !ok
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // A row tile is 32 weight rows as two M tiles of 16 (consecutive rows, or the same 16 rows of gate and up) of one
-// expert, times up to 8 NT of its tokens.  k_warps of the CTA's 8 warps share a row tile's chunks in turn,
-// the others take the next row tiles.  In a chunk the four lanes of a row take a unit of 32 codes each, all in
-// registers; the next chunk's words and grids (the next work item's at an item's end) are loaded while one is
-// worked on.  After each chunk the sums over its 128 columns are scaled into fp32 sums; at the end the
-// warps' sums are added in order through shared memory.
+// expert, times up to 8 NT of its tokens.  The CTA's 8 warps are k_warps groups: a group's warps take
+// neighbouring row tiles and the same chunks (every k_warps-th), so they share the tokens' terms; the groups'
+// sums are added in order through shared memory at the end.  Codes, grids, and tokens' terms arrive in a ring
+// of stages by asynchronous copies three chunks ahead, across the borders of work items, without holding
+// registers: with the next chunk in registers the same products took 2.3 us a chunk and warp, most of it waiting.
+// In a chunk the four lanes of a row take a unit of 32 codes each.  After each chunk the sums over its 128
+// columns are scaled into fp32 sums.
 // SUB: scales change inside a chunk (groups of 32 or 64); each quarter then has accumulators of its own and
 // sees the other quarters' tokens as zeros.
 template <int BITS, int TERMS, int NT, int SUB>
-__global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(const ProductArgs a) {
+__global__ void __launch_bounds__(kProductWarps * 32, (ctas_per_sm<NT, SUB>())) moe_product_kernel(const ProductArgs a) {
+  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float sums[kProductWarps][32][8 * NT + 1];
-  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  __shared__ uint16_t pair_of[kMaxPairs], row_of[kMaxPairs];  // pairs by expert; their rows of the terms
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int kw = warp & (a.k_warps - 1), rg = warp / a.k_warps;  // place among a row tile's warps; which row tile
-  const int groups = kProductWarps / a.k_warps;
+  const int groups = kProductWarps / a.k_warps;                  // row tiles of an item
+  const int kw = warp / groups, rg = warp - kw * groups;
   const int per_tile = (a.row_tiles + groups - 1) / groups;
   const int n_items = a.lists->n_tiles * per_tile;
   const bool gated = a.mode == kUpGated;
-  const uint32_t row_words = (uint32_t)a.units * BITS;
   const int tile_rows = gated ? 16 : 32;
+  const int64_t row_words = (int64_t)a.units * BITS;
+  if ((int)blockIdx.x >= n_items) return;
+  for (int i = threadIdx.x; i < a.pairs; i += kProductWarps * 32) {
+    const int p = a.lists->pairs[i];
+    pair_of[i] = (uint16_t)p;
+    row_of[i] = (uint16_t)(a.mode == kDown ? p : p / a.top_k);
+  }
+  __syncthreads();
 
-  // this warp's row tile of an item: the first row of M tile 0, and what M tile 1 adds to it (16 rows, or the
-  // way from gate to up)
-  const uint32_t* words;
-  const float* scales;
-  const int32_t* zeros;
-  const int64_t words1 = gated ? a.b.words - a.a.words : 16 * (int64_t)row_words;
-  const int64_t scales1 = gated ? a.b.scales - a.a.scales : 16 * (int64_t)a.ng;
-  const int64_t zeros1 = gated ? a.b.zeros - a.a.zeros : 16 * (int64_t)a.ng;
-  auto set_rows = [&](int item, int expert) {
-    const int64_t r = (int64_t)expert * a.rows + min(item % per_tile * groups + rg, a.row_tiles - 1) * tile_rows + g;
-    words = a.a.words + r * row_words + t * BITS;
-    scales = a.a.scales + r * a.ng;
-    zeros = a.a.zeros + r * a.ng;
-  };
-  uint32_t next[4][BITS];
-  float next_s[4];    // SUB > 1: of this lane's unit
-  int32_t next_z[4];
-  auto load = [&](int c) {
-    const bool ok = 4 * c + t < a.units;
-    const uint32_t* w = words + (uint32_t)c * (4 * BITS);
-    load_unit<BITS>(w, ok, next[0]);
-    load_unit<BITS>(w + 8 * row_words, ok, next[1]);
-    load_unit<BITS>(w + words1, ok, next[2]);
-    load_unit<BITS>(w + words1 + 8 * row_words, ok, next[3]);
-    const int grid = min(SUB == 1 ? 4 * c : 4 * c + t, a.units - 1) / a.group_units;
-    next_s[0] = __ldg(scales + grid), next_s[1] = __ldg(scales + grid + 8 * a.ng);
-    next_s[2] = __ldg(scales + grid + scales1), next_s[3] = __ldg(scales + grid + scales1 + 8 * a.ng);
-    next_z[0] = __ldg(zeros + grid), next_z[1] = __ldg(zeros + grid + 8 * a.ng);
-    next_z[2] = __ldg(zeros + grid + zeros1), next_z[3] = __ldg(zeros + grid + zeros1 + 8 * a.ng);
-  };
+  constexpr int WS = warp_stage_bytes<BITS, SUB>();
+  const int ts = token_stage_bytes(a.cols, TERMS, SUB);
+  const int stage_bytes = kProductWarps * WS + a.k_warps * ts;
+  const uint32_t ring0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const uint32_t ring_end = kStages * stage_bytes;
+  const int my_codes = warp * WS, my_tokens = kProductWarps * WS + kw * ts;
+  const int steps = a.chunks > kw ? (a.chunks - kw + a.k_warps - 1) / a.k_warps : 0;  // this group's chunks
 
-  int item = blockIdx.x;
-  if (item >= n_items) return;
-  set_rows(item, a.lists->tiles[item / per_tile].expert);
-  if (kw < a.chunks) load(kw);
-  for (; item < n_items; item += gridDim.x) {
+  // ---- the copies: chunk after chunk of item after item
+  const int gt = rg * 32 + lane, gn = groups * 32;  // this thread among its group's
+  int in_item = blockIdx.x, in_c = kw;
+  uint32_t in_stage = 0;
+  int in_first = 0, in_count = 0;
+  const uint32_t* words = nullptr;     // chunk in_c of the row tile's first row
+  const float* scales = nullptr;       // row `lane` of the tile
+  const int32_t* zeros = nullptr;
+  const uint16_t* token_src = nullptr;  // this thread's first piece of the tokens' terms, and of their sums
+  const float2* stat_src = nullptr;
+  // where this lane's pieces of the codes lie, from `words`: 3 bits in three runs of 16 bytes a row where rows
+  // start on 16 bytes, else the lane's own unit of its four rows
+  constexpr int NP = BITS == 3 ? 3 : 4;
+  const bool runs = BITS == 3 && (a.units & 3) == 0;
+  const int64_t words1 = gated ? a.b.words - a.a.words : 16 * row_words;  // from M tile 0 to M tile 1
+  int64_t piece[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int p = lane + 32 * i;
+    piece[i] = runs ? (p / 3 & 15) * row_words + (p / 48) * words1 + p % 3 * 4
+                    : (8 * (i & 1) + g) * row_words + (i >> 1) * words1 + t * BITS;
+  }
+  const uint32_t grid_magic = a.grid_magic;
+  auto grid_of = [&](int u) {  // u / group_units
+    return SUB > 1 ? u >> (a.group_units - 1) : (int)__umulhi((uint32_t)u, grid_magic);
+  };
+  auto begin_item = [&]() {
+    if (in_item >= n_items) return;
+    const Tile tile = a.lists->tiles[in_item / per_tile];
+    in_first = tile.first, in_count = tile.count;
+    const int64_t r = (int64_t)tile.expert * a.rows + min(in_item % per_tile * groups + rg, a.row_tiles - 1) * tile_rows;
+    words = a.a.words + r * row_words + kw * (4 * BITS);
+    const int64_t lane_row = (r + (gated ? lane & 15 : lane)) * a.ng;
+    scales = (gated && lane >= 16 ? a.b.scales : a.a.scales) + lane_row;
+    zeros = (gated && lane >= 16 ? a.b.zeros : a.a.zeros) + lane_row;
+    const int j = gt / (16 * TERMS), k = gt / 16 % TERMS;
+    if (j < in_count)
+      token_src = a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.chunks + kw) * 128 + (gt & 15) * 8;
+    if (gt < in_count) stat_src = a.terms.chunk + ((int64_t)row_of[in_first + gt] * a.chunks + kw);
+  };
+  auto issue = [&]() {
+    if (in_item < n_items && steps > 0) {
+      const uint32_t stage = ring0 + in_stage, codes = stage + my_codes;
+      const int c = in_c;
+      if constexpr (BITS == 3) {
+        if (runs) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) copy_async<16>(codes + (lane + 32 * i) * 16, words + piece[i]);
+        } else {
+          const bool ok = 4 * c + t < a.units;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              copy_async<4>(codes + ((8 * i + g) * 12 + t * 3 + k) * 4, ok ? words + piece[i] + k : words, ok);
+        }
+      } else {
+        const bool ok = 4 * c + t < a.units;
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          copy_async<4 * BITS>(codes + ((8 * i + g) * 4 + t) * (4 * BITS), ok ? words + piece[i] : words, ok);
+      }
+#pragma unroll
+      for (int s = 0; s < SUB; ++s) {
+        const int grid = grid_of(min(4 * c + s, a.units - 1));
+        copy_async<4>(codes + 512 * BITS + (lane * SUB + s) * 4, scales + grid);
+        copy_async<4>(codes + 512 * BITS + (32 * SUB + lane * SUB + s) * 4, zeros + grid);
+      }
+      // the group's threads share its tokens: 16 pieces per token and term, odd tokens' neighbouring quads exchanged
+      // so that two tokens' pieces of one quad lie in different banks
+      const uint32_t tokens = stage + my_tokens;
+      const int pieces = in_count * (16 * TERMS);
+      if (gt < pieces)
+        copy_async<16>(tokens + (gt >> 4) * 256 + ((gt & 15) ^ 4 * (gt / (16 * TERMS) & 1)) * 16, token_src);
+      for (int p = gt + gn; p < pieces; p += gn) {
+        const int j = p / (16 * TERMS), k = p / 16 % TERMS;
+        copy_async<16>(tokens + (p >> 4) * 256 + ((p & 15) ^ 4 * (j & 1)) * 16,
+                       a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.chunks + c) * 128 + (p & 15) * 8);
+      }
+      const uint32_t stats = tokens + a.cols * (TERMS * 256);
+      if (gt < in_count) {  // at most 16 tokens: the group's first warp
+        copy_async<8>(stats + gt * 8, stat_src);
+        if constexpr (SUB > 1) copy_async<16>(stats + a.cols * 16 + gt * 16, a.terms.unit + (stat_src - a.terms.chunk) * 4);
+      }
+      in_c += a.k_warps;
+      words += a.k_warps * (4 * BITS);
+      token_src += a.k_warps * 128;
+      stat_src += a.k_warps;
+      if (in_c >= a.chunks) {
+        in_c = kw;
+        in_item += gridDim.x;
+        begin_item();
+      }
+    }
+    copies_commit();
+    in_stage += stage_bytes;
+    if (in_stage == ring_end) in_stage = 0;
+  };
+  begin_item();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue();
+
+  uint32_t out_stage = 0;
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
     const int first = a.lists->tiles[item / per_tile].first, count = a.lists->tiles[item / per_tile].count;
-    const int next_item = item + gridDim.x;
-    const int next_expert = next_item < n_items ? a.lists->tiles[next_item / per_tile].expert : 0;
-    // entry g of every 8 tokens is this lane's column of B; entries 2 t and 2 t + 1 are its columns of the sums
-    constexpr uint32_t kNone = 0xffffffffu;
-    uint32_t tok[NT], col[NT][2];
+    // Columns past the tile's last token repeat it (nobody reads them).  This lane's column of B is entry g of every
+    // 8 (quad 0's piece; quad q's is that with q exchanged into its place), its columns of the sums are
+    // entries 2 t and 2 t + 1.
+    int tok[NT], col[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      auto row_at = [&](int i) {
-        const int p = a.lists->pairs[first + min(i, count - 1)];
-        return (uint32_t)(a.mode == kDown ? p : p / a.top_k) * (uint32_t)a.chunks;
-      };
-      tok[n] = 8 * n + g < count ? row_at(8 * n + g) * 128 + t * 32 : kNone;
-      col[n][0] = row_at(8 * n + 2 * t), col[n][1] = row_at(8 * n + 2 * t + 1);
+      const int j = min(8 * n + g, count - 1);
+      tok[n] = j * (TERMS * 256) + ((t ^ 4 * (j & 1)) << 4);
+      col[n][0] = min(8 * n + 2 * t, count - 1), col[n][1] = min(8 * n + 2 * t + 1, count - 1);
     }
     float acc[2][NT][4];
 #pragma unroll
@@ -537,42 +634,58 @@ __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(cons
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-    for (int c = kw; c < a.chunks; c += a.k_warps) {
+    for (int step = 0; step < steps; ++step) {
+      copies_wait<kStages - 2>();
+      // the group's copies of this stage have landed and its reads of the one before are done
+      if (groups == 1)
+        __syncwarp();
+      else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "r"(gn) : "memory");
+      issue();
+      const uint8_t* stage = ring + out_stage;
+      out_stage += stage_bytes;
+      if (out_stage == ring_end) out_stage = 0;
+      const uint32_t* codes = reinterpret_cast<const uint32_t*>(stage + my_codes);
       uint32_t w[4][BITS];
-      float sc[4], z[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const uint32_t* p = codes + ((8 * i + g) * 4 + t) * BITS;
+        if constexpr (BITS == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
+          w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+        } else if constexpr (BITS == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          w[i][0] = v.x, w[i][1] = v.y;
+        } else {
 #pragma unroll
-        for (int k = 0; k < BITS; ++k) w[i][k] = next[i][k];
-        sc[i] = next_s[i] * 16777216.0f, z[i] = -(float)next_z[i];
+          for (int k = 0; k < BITS; ++k) w[i][k] = p[k];
+        }
       }
-      if (c + a.k_warps < a.chunks) {
-        load(c + a.k_warps);
-      } else if (next_item < n_items) {
-        set_rows(next_item, next_expert);
-        load(kw);
-      }
-      const bool unit_here = 4 * c + t < a.units;
-      // lane s of the four holds the scale and the zero of quarter s
-      auto quarter = [&](float v, int s) { return SUB == 1 ? v : __shfl_sync(0xffffffffu, v, (lane & 28) | s); };
+      const float* sc = reinterpret_cast<const float*>(codes + 128 * BITS) + g * SUB;  // row g + 8 i: 8 SUB i further
+      const int32_t* zr = reinterpret_cast<const int32_t*>(codes + 128 * BITS) + 32 * SUB + g * SUB;
+      const uint8_t* tokens = stage + my_tokens;
+      const float2* stats = reinterpret_cast<const float2*>(tokens + a.cols * (TERMS * 256));
+      const float* unit_sums = reinterpret_cast<const float*>(tokens + a.cols * (TERMS * 256 + 16));
       // the accumulators start at -zero sum x; row g of an M tile is in values 0 and 1, row g + 8 in 2 and 3
       float sum[NT][SUB][2][4];
+      float2 st[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n == 0 || 8 * n < count) st[n][0] = stats[col[n][0]], st[n][1] = stats[col[n][1]];
 #pragma unroll
       for (int s = 0; s < SUB; ++s) {
-        const float zs[4] = {quarter(z[0], s), quarter(z[1], s), quarter(z[2], s), quarter(z[3], s)};
+        float z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = -(float)zr[8 * SUB * i + s];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (8 * n >= count) break;
-          float x0, x1;
-          if constexpr (SUB == 1) {
-            x0 = __ldg(&a.terms.chunk[col[n][0] + c].y), x1 = __ldg(&a.terms.chunk[col[n][1] + c].y);
-          } else {
-            x0 = __ldg(a.terms.unit + ((col[n][0] + c) * 4 + s)), x1 = __ldg(a.terms.unit + ((col[n][1] + c) * 4 + s));
-          }
+          if (n > 0 && 8 * n >= count) break;
+          const float x0 = SUB == 1 ? st[n][0].y : unit_sums[4 * col[n][0] + s];
+          const float x1 = SUB == 1 ? st[n][1].y : unit_sums[4 * col[n][1] + s];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            sum[n][s][m][0] = zs[2 * m] * x0, sum[n][s][m][1] = zs[2 * m] * x1;
-            sum[n][s][m][2] = zs[2 * m + 1] * x0, sum[n][s][m][3] = zs[2 * m + 1] * x1;
+            sum[n][s][m][0] = z[2 * m] * x0, sum[n][s][m][1] = z[2 * m] * x1;
+            sum[n][s][m][2] = z[2 * m + 1] * x0, sum[n][s][m][3] = z[2 * m + 1] * x1;
           }
         }
       }
@@ -583,12 +696,10 @@ __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(cons
         for (int i = 0; i < 4; ++i) unit_quad<BITS>(w[i], q, v[i]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (8 * n >= count) break;
+          if (n > 0 && 8 * n >= count) break;
 #pragma unroll
           for (int k = TERMS - 1; k >= 0; --k) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (tok[n] != kNone && unit_here)
-              x = __ldg(reinterpret_cast<const uint4*>(a.terms.values + k * a.terms.stride + (tok[n] + c * 128)) + q);
+            const uint4 x = *reinterpret_cast<const uint4*>(tokens + (tok[n] ^ (q & 1) << 6) + (q >> 1) * 128 + k * 256);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
 #pragma unroll
@@ -605,11 +716,13 @@ __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(cons
       }
 #pragma unroll
       for (int s = 0; s < SUB; ++s) {
-        const float ss[4] = {quarter(sc[0], s), quarter(sc[1], s), quarter(sc[2], s), quarter(sc[3], s)};
+        float ss[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss[i] = sc[8 * SUB * i + s];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (8 * n >= count) break;
-          const float e0 = __ldg(&a.terms.chunk[col[n][0] + c].x), e1 = __ldg(&a.terms.chunk[col[n][1] + c].x);
+          if (n > 0 && 8 * n >= count) break;
+          const float e0 = st[n][0].x, e1 = st[n][1].x;
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             acc[m][n][0] = fmaf(ss[2 * m] * e0, sum[n][s][m][0], acc[m][n][0]);
@@ -635,17 +748,19 @@ __global__ void __launch_bounds__(kProductWarps * 32, 2) moe_product_kernel(cons
       const int rt = item % per_tile * groups + j;
       if (rt >= a.row_tiles) continue;
       float v = 0.0f, up = 0.0f;
-      for (int w = j * a.k_warps; w < (j + 1) * a.k_warps; ++w) {
+      for (int w = j; w < kProductWarps; w += groups) {
         v += sums[w][r][n];
         if (gated) up += sums[w][16 + r][n];
       }
+      v *= kCodeInverse, up *= kCodeInverse;  // codes were taken as q 2^-24
       if (gated)
         v = v / (1.0f + expf(-v)) * up;
       else if (a.mode == kUpRelu)
         v = v < 0.0f ? 0.0f : v;  // NaN stays
-      a.out[(int64_t)a.lists->pairs[first + n] * a.rows + rt * tile_rows + r] = v;
+      a.out[(int64_t)pair_of[first + n] * a.rows + rt * tile_rows + r] = v;
     }
   }
+  copies_wait<0>();
 }
 
 // ------------------------------------------------------------------ weighted sum
@@ -676,35 +791,45 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const float* __restric
 }
 
 // ------------------------------------------------------------------ launches
-// warps per row tile: the fewest steps of a chunk along the longest chain of work items, an item's own
-// start and end counted as two steps
-int choose_k_warps(const ProductArgs& a, int tiles, int slots) {
-  int best = 8;
+// Groups per CTA (warps per row tile): the fewest chunk steps along the longest chain of work items, an item's own
+// start and end counted as two, among those whose stages leave room for the SM's other CTAs.
+template <int BITS, int TERMS, int NT, int SUB>
+int choose_k_warps(const ProductArgs& a, int tiles, int slots, int* smem) {
+  // an SM's 227 KB, less 1 KB and the static arrays of each CTA
+  constexpr int kRoom = 227 * 1024 / ctas_per_sm<NT, SUB>() - 1024 - kProductWarps * 32 * (8 * NT + 1) * 4 - 4 * kMaxPairs;
+  int best = 1;
   int64_t best_cost = INT64_MAX;
   for (int kw = 8; kw >= 1; kw /= 2) {
+    const int bytes = kStages * (kProductWarps * warp_stage_bytes<BITS, SUB>() + kw * token_stage_bytes(a.cols, TERMS, SUB));
     const int groups = kProductWarps / kw;
     const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
     const int64_t cost = (items + slots - 1) / slots * ((a.chunks + kw - 1) / kw + 2);
-    if (cost < best_cost) best = kw, best_cost = cost;
+    if (best_cost == INT64_MAX ? bytes <= kRoom || kw == 1 : bytes <= kRoom && cost < best_cost)
+      best = kw, best_cost = cost, *smem = bytes;
   }
   return best;
 }
 
-template <int BITS, int TERMS>
-gptq_status launch_product(ProductArgs a, int nt, bool sub, int tiles, int sms, cudaStream_t s) {
-  const int slots = 2 * sms;
-  a.k_warps = choose_k_warps(a, tiles, slots);
+template <int BITS, int TERMS, int NT, int SUB>
+gptq_status launch_product_form(ProductArgs a, int tiles, int sms, cudaStream_t s) {
+  const int slots = ctas_per_sm<NT, SUB>() * sms;
+  int smem = 0;
+  a.grid_magic = (uint32_t)(((1ull << 32) + a.group_units - 1) / a.group_units);  // not used for group_units 1
+  a.k_warps = choose_k_warps<BITS, TERMS, NT, SUB>(a, tiles, slots, &smem);
   const int groups = kProductWarps / a.k_warps;
   const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
-  const int grid = (int)std::min<int64_t>(items, slots);
-  if (sub)
-    moe_product_kernel<BITS, TERMS, 1, 4><<<grid, kProductWarps * 32, 0, s>>>(a);
-  else if (nt == 1)
-    moe_product_kernel<BITS, TERMS, 1, 1><<<grid, kProductWarps * 32, 0, s>>>(a);
-  else
-    moe_product_kernel<BITS, TERMS, 2, 1><<<grid, kProductWarps * 32, 0, s>>>(a);
+  auto kernel = moe_product_kernel<BITS, TERMS, NT, SUB>;
+  GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  kernel<<<(int)std::min<int64_t>(items, slots), kProductWarps * 32, smem, s>>>(a);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
+}
+
+template <int BITS, int TERMS>
+gptq_status launch_product(const ProductArgs& a, int nt, bool sub, int tiles, int sms, cudaStream_t s) {
+  if (sub) return launch_product_form<BITS, TERMS, 1, 4>(a, tiles, sms, s);
+  return nt == 1 ? launch_product_form<BITS, TERMS, 1, 1>(a, tiles, sms, s)
+                 : launch_product_form<BITS, TERMS, 2, 1>(a, tiles, sms, s);
 }
 
 template <typename T, int BITS, int TERMS>
@@ -760,7 +885,8 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   a.ng = m.group_size ? d / m.group_size : 1;
   a.group_units = m.group_size ? m.group_size / 32 : a.units;
   a.chunks = x_terms.chunks, a.row_tiles = m.gated ? f / 16 : f / 32;
-  a.top_k = m.top_k;
+  a.top_k = m.top_k, a.pairs = pairs;
+  a.cols = std::min(tile_tokens, m.router ? tokens : pairs);
   a.terms = x_terms;
   a.lists = lists;
   a.out = acts;
