@@ -139,7 +139,7 @@ struct Terms {
 struct Layout {
   size_t lists, logits, x_terms, a_terms, acts, products, total;
 };
-int chunks_of(int64_t cols) { return (int)((cols + 127) / 128); }
+int chunks_of(int64_t cols) { return (int)((cols + 255) / 256 * 2); }  // whole spans of two
 size_t terms_bytes(int64_t rows, int64_t cols) {
   return (size_t)rows * chunks_of(cols) * (2 * 256 + sizeof(float2) + 4 * sizeof(float));
 }
@@ -430,7 +430,9 @@ struct ProductArgs {
   int mode, rows, units;   // rows per expert, units of 32 columns per row
   int ng, group_units;     // grids per row, units per grid
   uint32_t grid_magic;     // ceil(2^32 / group_units): u / group_units in the high word, exact for u < 2^16
-  int chunks;              // 128-column chunks
+  int spans;               // of 256 columns, two chunks
+  bool wide_rows;          // rows of codes start on 16 bytes
+  bool grid_pairs;         // a span's two grids are neighbours and start on 8 bytes
   int row_tiles;           // 32-row (gated: 16-row) tiles of an expert
   int k_warps;             // warps that share a row tile's chunks: 1, 2, 4 or 8
   int cols;                // tokens of a tile at most
@@ -441,22 +443,29 @@ struct ProductArgs {
 };
 
 constexpr int kProductWarps = 8;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr float kCodeInverse = 16777216.0f;  // 2^24
 
-// CTAs on an SM: registers (80 or 128 a thread) and shared memory are held to it
-template <int NT, int SUB>
-__host__ __device__ constexpr int ctas_per_sm() {
-  return NT == 1 && SUB == 1 ? 3 : 2;
-}
+constexpr int kCtasPerSm = 2;  // registers (128 a thread) and shared memory are held to it
 
-// shared memory of one stage: every warp's codes and grids, every group's tokens (see moe_product_kernel)
+// Shared memory of one stage, a span of 256 columns: every warp's codes and grids, every group's tokens.
+// A row's codes of a span take 128, 96 or 64 bytes; their 16-byte pieces are laid out so that the 8 rows of an
+// M tile's half fall into different banks when each lane reads its unit: 3 bits by a row stride of 112 bytes, 4 and 2
+// bits by exchanging the halves of every second row, or of every second pair of rows (half_bit).
+template <int BITS>
+__host__ __device__ constexpr int code_stride() {
+  return BITS == 3 ? 112 : 32 * BITS;
+}
+template <int BITS>
+__host__ __device__ constexpr int half_bit(int row) {
+  return BITS == 4 ? row & 1 : (BITS == 2 ? row >> 1 & 1 : 0);
+}
 template <int BITS, int SUB>
 __host__ __device__ constexpr int warp_stage_bytes() {
-  return 512 * BITS + 2 * 32 * SUB * 4;
+  return 32 * code_stride<BITS>() + 2 * 32 * 2 * SUB * 4;
 }
 __host__ __device__ inline int token_stage_bytes(int cols, int terms, int sub) {
-  return cols * (terms * 256 + 16 + (sub > 1 ? 16 : 0));
+  return cols * (terms * 512 + 16 + (sub > 1 ? 32 : 0));
 }
 
 template <int N>
@@ -474,16 +483,16 @@ __device__ __forceinline__ void copies_wait() {
 
 // A row tile is 32 weight rows as two M tiles of 16 (consecutive rows, or the same 16 rows of gate and up) of one
 // expert, times up to 8 NT of its tokens.  The CTA's 8 warps are k_warps groups: a group's warps take
-// neighbouring row tiles and the same chunks (every k_warps-th), so they share the tokens' terms; the groups'
+// neighbouring row tiles and the same spans (every k_warps-th), so they share the tokens' terms; the groups'
 // sums are added in order through shared memory at the end.  Codes, grids, and tokens' terms arrive in a ring
-// of stages by asynchronous copies three chunks ahead, across the borders of work items, without holding
+// of stages by asynchronous copies a span of two chunks ahead, across the borders of work items, without holding
 // registers: with the next chunk in registers the same products took 2.3 us a chunk and warp, most of it waiting.
 // In a chunk the four lanes of a row take a unit of 32 codes each.  After each chunk the sums over its 128
 // columns are scaled into fp32 sums.
 // SUB: scales change inside a chunk (groups of 32 or 64); each quarter then has accumulators of its own and
 // sees the other quarters' tokens as zeros.
 template <int BITS, int TERMS, int NT, int SUB>
-__global__ void __launch_bounds__(kProductWarps * 32, (ctas_per_sm<NT, SUB>())) moe_product_kernel(const ProductArgs a) {
+__global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_kernel(const ProductArgs a) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float sums[kProductWarps][32][8 * NT + 1];
   __shared__ uint16_t pair_of[kMaxPairs], row_of[kMaxPairs];  // pairs by expert; their rows of the terms
@@ -505,35 +514,35 @@ __global__ void __launch_bounds__(kProductWarps * 32, (ctas_per_sm<NT, SUB>())) 
   __syncthreads();
 
   constexpr int WS = warp_stage_bytes<BITS, SUB>();
+  constexpr int RS = code_stride<BITS>(), HB = 16 * BITS;  // bytes of a row; of a row's half of a span
   const int ts = token_stage_bytes(a.cols, TERMS, SUB);
   const int stage_bytes = kProductWarps * WS + a.k_warps * ts;
   const uint32_t ring0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const uint32_t ring_end = kStages * stage_bytes;
   const int my_codes = warp * WS, my_tokens = kProductWarps * WS + kw * ts;
-  const int steps = a.chunks > kw ? (a.chunks - kw + a.k_warps - 1) / a.k_warps : 0;  // this group's chunks
+  const int steps = a.spans > kw ? (a.spans - kw + a.k_warps - 1) / a.k_warps : 0;  // this group's spans
 
-  // ---- the copies: chunk after chunk of item after item
+  // ---- the copies: span after span of item after item
   const int gt = rg * 32 + lane, gn = groups * 32;  // this thread among its group's
   int in_item = blockIdx.x, in_c = kw;
   uint32_t in_stage = 0;
   int in_first = 0, in_count = 0;
-  const uint32_t* words = nullptr;     // chunk in_c of the row tile's first row
+  const uint32_t* words = nullptr;     // span in_c of the row tile's first row
   const float* scales = nullptr;       // row `lane` of the tile
   const int32_t* zeros = nullptr;
   const uint16_t* token_src = nullptr;  // this thread's first piece of the tokens' terms, and of their sums
   const float2* stat_src = nullptr;
-  // where this lane's pieces of the codes lie, from `words`: 3 bits in three runs of 16 bytes a row where rows
-  // start on 16 bytes, else the lane's own unit of its four rows
-  constexpr int NP = BITS == 3 ? 3 : 4;
-  const bool runs = BITS == 3 && (a.units & 3) == 0;
   const int64_t words1 = gated ? a.b.words - a.a.words : 16 * row_words;  // from M tile 0 to M tile 1
-  int64_t piece[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int p = lane + 32 * i;
-    piece[i] = runs ? (p / 3 & 15) * row_words + (p / 48) * words1 + p % 3 * 4
-                    : (8 * (i & 1) + g) * row_words + (i >> 1) * words1 + t * BITS;
-  }
+  // this lane's 16-byte pieces of the codes: piece p = lane + 32 i is piece p % PP of row p / PP
+  constexpr int PP = 2 * BITS;
+  auto piece_src = [&](int p) {
+    const int row = p / PP;
+    return (row & 15) * row_words + (row >> 4) * words1 + p % PP * 4;
+  };
+  auto piece_dst = [&](int p) {
+    const int row = p / PP, at = p % PP;
+    return row * RS + (BITS == 3 ? at : at ^ (half_bit<BITS>(row) * BITS)) * 16;
+  };
   const uint32_t grid_magic = a.grid_magic;
   auto grid_of = [&](int u) {  // u / group_units
     return SUB > 1 ? u >> (a.group_units - 1) : (int)__umulhi((uint32_t)u, grid_magic);
@@ -543,64 +552,76 @@ __global__ void __launch_bounds__(kProductWarps * 32, (ctas_per_sm<NT, SUB>())) 
     const Tile tile = a.lists->tiles[in_item / per_tile];
     in_first = tile.first, in_count = tile.count;
     const int64_t r = (int64_t)tile.expert * a.rows + min(in_item % per_tile * groups + rg, a.row_tiles - 1) * tile_rows;
-    words = a.a.words + r * row_words + kw * (4 * BITS);
+    words = a.a.words + r * row_words + kw * (8 * BITS);
     const int64_t lane_row = (r + (gated ? lane & 15 : lane)) * a.ng;
     scales = (gated && lane >= 16 ? a.b.scales : a.a.scales) + lane_row;
     zeros = (gated && lane >= 16 ? a.b.zeros : a.a.zeros) + lane_row;
-    const int j = gt / (16 * TERMS), k = gt / 16 % TERMS;
+    const int j = gt / (32 * TERMS), k = gt / 32 % TERMS;
     if (j < in_count)
-      token_src = a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.chunks + kw) * 128 + (gt & 15) * 8;
-    if (gt < in_count) stat_src = a.terms.chunk + ((int64_t)row_of[in_first + gt] * a.chunks + kw);
+      token_src = a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.terms.chunks + 2 * kw) * 128 + (gt & 31) * 8;
+    if (gt < in_count) stat_src = a.terms.chunk + ((int64_t)row_of[in_first + gt] * a.terms.chunks + 2 * kw);
   };
   auto issue = [&]() {
     if (in_item < n_items && steps > 0) {
       const uint32_t stage = ring0 + in_stage, codes = stage + my_codes;
       const int c = in_c;
-      if constexpr (BITS == 3) {
-        if (runs) {
+      const int left = (int)row_words - c * (8 * BITS);  // words of a row from here on
+      if (BITS == 4 || a.wide_rows) {
+        if (left >= 8 * BITS) {
 #pragma unroll
-          for (int i = 0; i < NP; ++i) copy_async<16>(codes + (lane + 32 * i) * 16, words + piece[i]);
+          for (int i = 0; i < PP; ++i) copy_async<16>(codes + piece_dst(lane + 32 * i), words + piece_src(lane + 32 * i));
         } else {
-          const bool ok = 4 * c + t < a.units;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              copy_async<4>(codes + ((8 * i + g) * 12 + t * 3 + k) * 4, ok ? words + piece[i] + k : words, ok);
+          for (int i = 0; i < PP; ++i) {
+            const int p = lane + 32 * i;
+            const bool ok = p % PP * 4 < left;
+            copy_async<16>(codes + piece_dst(p), ok ? words + piece_src(p) : words, ok);
+          }
         }
+      } else {  // rows on any 4 bytes: word by word
+#pragma unroll 1
+        for (int p = lane; p < 32 * PP * 4; p += 32) {
+          const bool ok = (p / 4) % PP * 4 + p % 4 < left;
+          copy_async<4>(codes + piece_dst(p / 4) + p % 4 * 4, ok ? words + piece_src(p / 4) + p % 4 : words, ok);
+        }
+      }
+      const uint32_t grids = codes + 32 * RS + lane * (2 * SUB * 4);  // [row][chunk, quarter] scales, then zeros
+      if (SUB == 1 && a.grid_pairs) {
+        copy_async<8>(grids, scales + 2 * c);
+        copy_async<8>(grids + 32 * 2 * 4, zeros + 2 * c);
       } else {
-        const bool ok = 4 * c + t < a.units;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          copy_async<4 * BITS>(codes + ((8 * i + g) * 4 + t) * (4 * BITS), ok ? words + piece[i] : words, ok);
+        for (int s = 0; s < 2 * SUB; ++s) {
+          const int grid = grid_of(min(8 * c + (SUB == 1 ? 4 * s : s), a.units - 1));
+          copy_async<4>(grids + s * 4, scales + grid);
+          copy_async<4>(grids + (32 * 2 * SUB + s) * 4, zeros + grid);
+        }
       }
-#pragma unroll
-      for (int s = 0; s < SUB; ++s) {
-        const int grid = grid_of(min(4 * c + s, a.units - 1));
-        copy_async<4>(codes + 512 * BITS + (lane * SUB + s) * 4, scales + grid);
-        copy_async<4>(codes + 512 * BITS + (32 * SUB + lane * SUB + s) * 4, zeros + grid);
-      }
-      // the group's threads share its tokens: 16 pieces per token and term, odd tokens' neighbouring quads exchanged
+      // the group's threads share its tokens: 32 pieces per token and term, odd tokens' neighbouring quads exchanged
       // so that two tokens' pieces of one quad lie in different banks
       const uint32_t tokens = stage + my_tokens;
-      const int pieces = in_count * (16 * TERMS);
+      const int pieces = in_count * (32 * TERMS);
       if (gt < pieces)
-        copy_async<16>(tokens + (gt >> 4) * 256 + ((gt & 15) ^ 4 * (gt / (16 * TERMS) & 1)) * 16, token_src);
+        copy_async<16>(tokens + (gt >> 5) * 512 + ((gt & 31) ^ 4 * (gt / (32 * TERMS) & 1)) * 16, token_src);
       for (int p = gt + gn; p < pieces; p += gn) {
-        const int j = p / (16 * TERMS), k = p / 16 % TERMS;
-        copy_async<16>(tokens + (p >> 4) * 256 + ((p & 15) ^ 4 * (j & 1)) * 16,
-                       a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.chunks + c) * 128 + (p & 15) * 8);
+        const int j = p / (32 * TERMS), k = p / 32 % TERMS;
+        copy_async<16>(tokens + (p >> 5) * 512 + ((p & 31) ^ 4 * (j & 1)) * 16,
+                       a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.terms.chunks + 2 * c) * 128 + (p & 31) * 8);
       }
-      const uint32_t stats = tokens + a.cols * (TERMS * 256);
+      const uint32_t stats = tokens + a.cols * (TERMS * 512);
       if (gt < in_count) {  // at most 16 tokens: the group's first warp
-        copy_async<8>(stats + gt * 8, stat_src);
-        if constexpr (SUB > 1) copy_async<16>(stats + a.cols * 16 + gt * 16, a.terms.unit + (stat_src - a.terms.chunk) * 4);
+        copy_async<16>(stats + gt * 16, stat_src);
+        if constexpr (SUB > 1) {
+          const float* units = a.terms.unit + (stat_src - a.terms.chunk) * 4;
+          copy_async<16>(stats + a.cols * 16 + gt * 32, units);
+          copy_async<16>(stats + a.cols * 16 + gt * 32 + 16, units + 4);
+        }
       }
       in_c += a.k_warps;
-      words += a.k_warps * (4 * BITS);
-      token_src += a.k_warps * 128;
-      stat_src += a.k_warps;
-      if (in_c >= a.chunks) {
+      words += a.k_warps * (8 * BITS);
+      token_src += a.k_warps * 256;
+      stat_src += a.k_warps * 2;
+      if (in_c >= a.spans) {
         in_c = kw;
         in_item += gridDim.x;
         begin_item();
@@ -624,7 +645,7 @@ __global__ void __launch_bounds__(kProductWarps * 32, (ctas_per_sm<NT, SUB>())) 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int j = min(8 * n + g, count - 1);
-      tok[n] = j * (TERMS * 256) + ((t ^ 4 * (j & 1)) << 4);
+      tok[n] = j * (TERMS * 512) + ((t ^ 4 * (j & 1)) << 4);
       col[n][0] = min(8 * n + 2 * t, count - 1), col[n][1] = min(8 * n + 2 * t + 1, count - 1);
     }
     float acc[2][NT][4];
@@ -645,90 +666,94 @@ __global__ void __launch_bounds__(kProductWarps * 32, (ctas_per_sm<NT, SUB>())) 
       const uint8_t* stage = ring + out_stage;
       out_stage += stage_bytes;
       if (out_stage == ring_end) out_stage = 0;
-      const uint32_t* codes = reinterpret_cast<const uint32_t*>(stage + my_codes);
-      uint32_t w[4][BITS];
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {  // the span's chunks
+        const uint8_t* codes = stage + my_codes;
+        uint32_t w[4][BITS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t* p = codes + ((8 * i + g) * 4 + t) * BITS;
-        if constexpr (BITS == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p);
-          w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
-        } else if constexpr (BITS == 2) {
-          const uint2 v = *reinterpret_cast<const uint2*>(p);
-          w[i][0] = v.x, w[i][1] = v.y;
-        } else {
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(codes + (8 * i + g) * RS + (h ^ half_bit<BITS>(g)) * HB + t * (4 * BITS));
+          if constexpr (BITS == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+          } else if constexpr (BITS == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[i][0] = v.x, w[i][1] = v.y;
+          } else {
 #pragma unroll
-          for (int k = 0; k < BITS; ++k) w[i][k] = p[k];
-        }
-      }
-      const float* sc = reinterpret_cast<const float*>(codes + 128 * BITS) + g * SUB;  // row g + 8 i: 8 SUB i further
-      const int32_t* zr = reinterpret_cast<const int32_t*>(codes + 128 * BITS) + 32 * SUB + g * SUB;
-      const uint8_t* tokens = stage + my_tokens;
-      const float2* stats = reinterpret_cast<const float2*>(tokens + a.cols * (TERMS * 256));
-      const float* unit_sums = reinterpret_cast<const float*>(tokens + a.cols * (TERMS * 256 + 16));
-      // the accumulators start at -zero sum x; row g of an M tile is in values 0 and 1, row g + 8 in 2 and 3
-      float sum[NT][SUB][2][4];
-      float2 st[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n == 0 || 8 * n < count) st[n][0] = stats[col[n][0]], st[n][1] = stats[col[n][1]];
-#pragma unroll
-      for (int s = 0; s < SUB; ++s) {
-        float z[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = -(float)zr[8 * SUB * i + s];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n > 0 && 8 * n >= count) break;
-          const float x0 = SUB == 1 ? st[n][0].y : unit_sums[4 * col[n][0] + s];
-          const float x1 = SUB == 1 ? st[n][1].y : unit_sums[4 * col[n][1] + s];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            sum[n][s][m][0] = z[2 * m] * x0, sum[n][s][m][1] = z[2 * m] * x1;
-            sum[n][s][m][2] = z[2 * m + 1] * x0, sum[n][s][m][3] = z[2 * m + 1] * x1;
+            for (int k = 0; k < BITS; ++k) w[i][k] = p[k];
           }
         }
-      }
+        // row g + 8 i: 16 SUB i further
+        const float* sc = reinterpret_cast<const float*>(codes + 32 * RS) + g * (2 * SUB) + h * SUB;
+        const int32_t* zr = reinterpret_cast<const int32_t*>(codes + 32 * RS) + 32 * 2 * SUB + g * (2 * SUB) + h * SUB;
+        const uint8_t* tokens = stage + my_tokens + h * 256;
+        const float2* stats = reinterpret_cast<const float2*>(stage + my_tokens + a.cols * (TERMS * 512)) + h;
+        const float* unit_sums = reinterpret_cast<const float*>(stage + my_tokens + a.cols * (TERMS * 512 + 16)) + h * 4;
+        // the accumulators start at -zero sum x; row g of an M tile is in values 0 and 1, row g + 8 in 2 and 3
+        float sum[NT][SUB][2][4];
+        float2 st[NT][2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // registers 4 q .. 4 q + 3 of the units: 32 of the chunk's columns
-        uint32_t v[4][4];
+        for (int n = 0; n < NT; ++n)
+          if (n == 0 || 8 * n < count) st[n][0] = stats[2 * col[n][0]], st[n][1] = stats[2 * col[n][1]];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) unit_quad<BITS>(w[i], q, v[i]);
+        for (int s = 0; s < SUB; ++s) {
+          float z[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n > 0 && 8 * n >= count) break;
+          for (int i = 0; i < 4; ++i) z[i] = -(float)zr[16 * SUB * i + s];
 #pragma unroll
-          for (int k = TERMS - 1; k >= 0; --k) {
-            const uint4 x = *reinterpret_cast<const uint4*>(tokens + (tok[n] ^ (q & 1) << 6) + (q >> 1) * 128 + k * 256);
+          for (int n = 0; n < NT; ++n) {
+            if (n > 0 && 8 * n >= count) break;
+            const float x0 = SUB == 1 ? st[n][0].y : unit_sums[8 * col[n][0] + s];
+            const float x1 = SUB == 1 ? st[n][1].y : unit_sums[8 * col[n][1] + s];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
+              sum[n][s][m][0] = z[2 * m] * x0, sum[n][s][m][1] = z[2 * m] * x1;
+              sum[n][s][m][2] = z[2 * m + 1] * x0, sum[n][s][m][3] = z[2 * m + 1] * x1;
+            }
+          }
+        }
 #pragma unroll
-              for (int s = 0; s < SUB; ++s) {
-                const bool mine = SUB == 1 || t == s;
-                mma_f16(sum[n][s][m], v[2 * m][0], v[2 * m + 1][0], v[2 * m][1], v[2 * m + 1][1], mine ? x.x : 0u,
-                        mine ? x.y : 0u);
-                mma_f16(sum[n][s][m], v[2 * m][2], v[2 * m + 1][2], v[2 * m][3], v[2 * m + 1][3], mine ? x.z : 0u,
-                        mine ? x.w : 0u);
+        for (int q = 0; q < 4; ++q) {  // registers 4 q .. 4 q + 3 of the units: 32 of the chunk's columns
+          uint32_t v[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) unit_quad<BITS>(w[i], q, v[i]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (n > 0 && 8 * n >= count) break;
+#pragma unroll
+            for (int k = TERMS - 1; k >= 0; --k) {
+              const uint4 x = *reinterpret_cast<const uint4*>(tokens + (tok[n] ^ (q & 1) << 6) + (q >> 1) * 128 + k * 512);
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                for (int s = 0; s < SUB; ++s) {
+                  const bool mine = SUB == 1 || t == s;
+                  mma_f16(sum[n][s][m], v[2 * m][0], v[2 * m + 1][0], v[2 * m][1], v[2 * m + 1][1], mine ? x.x : 0u,
+                          mine ? x.y : 0u);
+                  mma_f16(sum[n][s][m], v[2 * m][2], v[2 * m + 1][2], v[2 * m][3], v[2 * m + 1][3], mine ? x.z : 0u,
+                          mine ? x.w : 0u);
+                }
               }
             }
           }
         }
-      }
 #pragma unroll
-      for (int s = 0; s < SUB; ++s) {
-        float ss[4];
+        for (int s = 0; s < SUB; ++s) {
+          float ss[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ss[i] = sc[8 * SUB * i + s];
+          for (int i = 0; i < 4; ++i) ss[i] = sc[16 * SUB * i + s];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n > 0 && 8 * n >= count) break;
-          const float e0 = st[n][0].x, e1 = st[n][1].x;
+          for (int n = 0; n < NT; ++n) {
+            if (n > 0 && 8 * n >= count) break;
+            const float e0 = st[n][0].x, e1 = st[n][1].x;
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            acc[m][n][0] = fmaf(ss[2 * m] * e0, sum[n][s][m][0], acc[m][n][0]);
-            acc[m][n][1] = fmaf(ss[2 * m] * e1, sum[n][s][m][1], acc[m][n][1]);
-            acc[m][n][2] = fmaf(ss[2 * m + 1] * e0, sum[n][s][m][2], acc[m][n][2]);
-            acc[m][n][3] = fmaf(ss[2 * m + 1] * e1, sum[n][s][m][3], acc[m][n][3]);
+            for (int m = 0; m < 2; ++m) {
+              acc[m][n][0] = fmaf(ss[2 * m] * e0, sum[n][s][m][0], acc[m][n][0]);
+              acc[m][n][1] = fmaf(ss[2 * m] * e1, sum[n][s][m][1], acc[m][n][1]);
+              acc[m][n][2] = fmaf(ss[2 * m + 1] * e0, sum[n][s][m][2], acc[m][n][2]);
+              acc[m][n][3] = fmaf(ss[2 * m + 1] * e1, sum[n][s][m][3], acc[m][n][3]);
+            }
           }
         }
       }
@@ -791,19 +816,19 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const float* __restric
 }
 
 // ------------------------------------------------------------------ launches
-// Groups per CTA (warps per row tile): the fewest chunk steps along the longest chain of work items, an item's own
-// start and end counted as two, among those whose stages leave room for the SM's other CTAs.
+// Groups per CTA (warps per row tile): the fewest span steps along the longest chain of work items, an item's own
+// start and end counted as one, among those whose stages leave room for the SM's other CTAs.
 template <int BITS, int TERMS, int NT, int SUB>
 int choose_k_warps(const ProductArgs& a, int tiles, int slots, int* smem) {
   // an SM's 227 KB, less 1 KB and the static arrays of each CTA
-  constexpr int kRoom = 227 * 1024 / ctas_per_sm<NT, SUB>() - 1024 - kProductWarps * 32 * (8 * NT + 1) * 4 - 4 * kMaxPairs;
+  constexpr int kRoom = 227 * 1024 / kCtasPerSm - 1024 - kProductWarps * 32 * (8 * NT + 1) * 4 - 4 * kMaxPairs;
   int best = 1;
   int64_t best_cost = INT64_MAX;
   for (int kw = 8; kw >= 1; kw /= 2) {
     const int bytes = kStages * (kProductWarps * warp_stage_bytes<BITS, SUB>() + kw * token_stage_bytes(a.cols, TERMS, SUB));
     const int groups = kProductWarps / kw;
     const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
-    const int64_t cost = (items + slots - 1) / slots * ((a.chunks + kw - 1) / kw + 2);
+    const int64_t cost = (items + slots - 1) / slots * ((a.spans + kw - 1) / kw + 1);
     if (best_cost == INT64_MAX ? bytes <= kRoom || kw == 1 : bytes <= kRoom && cost < best_cost)
       best = kw, best_cost = cost, *smem = bytes;
   }
@@ -812,8 +837,11 @@ int choose_k_warps(const ProductArgs& a, int tiles, int slots, int* smem) {
 
 template <int BITS, int TERMS, int NT, int SUB>
 gptq_status launch_product_form(ProductArgs a, int tiles, int sms, cudaStream_t s) {
-  const int slots = ctas_per_sm<NT, SUB>() * sms;
+  const int slots = kCtasPerSm * sms;
   int smem = 0;
+  a.wide_rows = a.units * BITS % 4 == 0;
+  auto pairs_of = [&](const Matrix& w) { return aligned(w.scales, 8) && aligned(w.zeros, 8); };
+  a.grid_pairs = a.group_units == 4 && a.ng % 2 == 0 && pairs_of(a.a) && (a.mode != kUpGated || pairs_of(a.b));
   a.grid_magic = (uint32_t)(((1ull << 32) + a.group_units - 1) / a.group_units);  // not used for group_units 1
   a.k_warps = choose_k_warps<BITS, TERMS, NT, SUB>(a, tiles, slots, &smem);
   const int groups = kProductWarps / a.k_warps;
@@ -884,7 +912,7 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   a.rows = f, a.units = d / 32;
   a.ng = m.group_size ? d / m.group_size : 1;
   a.group_units = m.group_size ? m.group_size / 32 : a.units;
-  a.chunks = x_terms.chunks, a.row_tiles = m.gated ? f / 16 : f / 32;
+  a.spans = x_terms.chunks / 2, a.row_tiles = m.gated ? f / 16 : f / 32;
   a.top_k = m.top_k, a.pairs = pairs;
   a.cols = std::min(tile_tokens, m.router ? tokens : pairs);
   a.terms = x_terms;
@@ -903,7 +931,7 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   a.rows = d, a.units = f / 32;
   a.ng = m.group_size ? f / m.group_size : 1;
   a.group_units = m.group_size ? m.group_size / 32 : a.units;
-  a.chunks = a_terms.chunks, a.row_tiles = d / 32;
+  a.spans = a_terms.chunks / 2, a.row_tiles = d / 32;
   a.terms = a_terms;
   a.out = products;
   st = a_wide ? launch_product<BITS, 2>(a, nt, sub, tiles, sms, s) : launch_product<BITS, 1>(a, nt, sub, tiles, sms, s);
