@@ -501,11 +501,10 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
   const int groups = kProductWarps / a.k_warps;                  // row tiles of an item
   const int kw = warp / groups, rg = warp - kw * groups;
   const int per_tile = (a.row_tiles + groups - 1) / groups;
-  const int n_items = a.lists->n_tiles * per_tile;
   const bool gated = a.mode == kUpGated;
   const int tile_rows = gated ? 16 : 32;
   const int64_t row_words = (int64_t)a.units * BITS;
-  if ((int)blockIdx.x >= n_items) return;
+  if ((int)blockIdx.x >= a.lists->n_tiles * per_tile) return;
   for (int i = threadIdx.x; i < a.pairs; i += kProductWarps * 32) {
     const int p = a.lists->pairs[i];
     pair_of[i] = (uint16_t)p;
@@ -524,35 +523,42 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
 
   // ---- the copies: span after span of item after item
   const int gt = rg * 32 + lane, gn = groups * 32;  // this thread among its group's
-  int in_item = blockIdx.x, in_c = kw;
+  // an item is row tiles in_rt .. of list tile in_tile; the next one lies gridDim.x items further on
+  const int hop_tile = (int)gridDim.x / per_tile, hop_rt = (int)gridDim.x % per_tile;
+  auto hop = [&](int& tile, int& rt) {
+    tile += hop_tile, rt += hop_rt;
+    if (rt >= per_tile) rt -= per_tile, ++tile;
+  };
+  int in_tile = (int)blockIdx.x / per_tile, in_rt = (int)blockIdx.x % per_tile, in_c = kw;
+  const int n_tiles = a.lists->n_tiles;
   uint32_t in_stage = 0;
   int in_first = 0, in_count = 0;
-  const uint32_t* words = nullptr;     // span in_c of the row tile's first row
+  const uint32_t *words0 = nullptr, *words1 = nullptr;  // span in_c of the M tiles' first rows
   const float* scales = nullptr;       // row `lane` of the tile
   const int32_t* zeros = nullptr;
   const uint16_t* token_src = nullptr;  // this thread's first piece of the tokens' terms, and of their sums
   const float2* stat_src = nullptr;
-  const int64_t words1 = gated ? a.b.words - a.a.words : 16 * row_words;  // from M tile 0 to M tile 1
-  // this lane's 16-byte pieces of the codes: piece p = lane + 32 i is piece p % PP of row p / PP
-  constexpr int PP = 2 * BITS;
-  auto piece_src = [&](int p) {
-    const int row = p / PP;
-    return (row & 15) * row_words + (row >> 4) * words1 + p % PP * 4;
-  };
-  auto piece_dst = [&](int p) {
-    const int row = p / PP, at = p % PP;
-    return row * RS + (BITS == 3 ? at : at ^ (half_bit<BITS>(row) * BITS)) * 16;
-  };
+  // This lane's 16-byte pieces of an M tile's codes: piece p = lane + 32 i is piece p % PP of row p / PP.  From
+  // the tile's first row to them, in words and in bytes of the stage:
+  constexpr int PP = 2 * BITS, NI = 16 * PP / 32;
+  int src_of[NI], dst_of[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int row = (lane + 32 * i) / PP, at = (lane + 32 * i) % PP;
+    src_of[i] = row * (int)row_words + at * 4;
+    dst_of[i] = row * RS + (at ^ (half_bit<BITS>(row) * BITS)) * 16;
+  }
   const uint32_t grid_magic = a.grid_magic;
   auto grid_of = [&](int u) {  // u / group_units
     return SUB > 1 ? u >> (a.group_units - 1) : (int)__umulhi((uint32_t)u, grid_magic);
   };
   auto begin_item = [&]() {
-    if (in_item >= n_items) return;
-    const Tile tile = a.lists->tiles[in_item / per_tile];
+    if (in_tile >= n_tiles) return;
+    const Tile tile = a.lists->tiles[in_tile];
     in_first = tile.first, in_count = tile.count;
-    const int64_t r = (int64_t)tile.expert * a.rows + min(in_item % per_tile * groups + rg, a.row_tiles - 1) * tile_rows;
-    words = a.a.words + r * row_words + kw * (8 * BITS);
+    const int64_t r = (int64_t)tile.expert * a.rows + min(in_rt * groups + rg, a.row_tiles - 1) * tile_rows;
+    words0 = a.a.words + r * row_words + kw * (8 * BITS);
+    words1 = gated ? a.b.words + r * row_words + kw * (8 * BITS) : words0 + 16 * row_words;
     const int64_t lane_row = (r + (gated ? lane & 15 : lane)) * a.ng;
     scales = (gated && lane >= 16 ? a.b.scales : a.a.scales) + lane_row;
     zeros = (gated && lane >= 16 ? a.b.zeros : a.a.zeros) + lane_row;
@@ -562,27 +568,23 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
     if (gt < in_count) stat_src = a.terms.chunk + ((int64_t)row_of[in_first + gt] * a.terms.chunks + 2 * kw);
   };
   auto issue = [&]() {
-    if (in_item < n_items && steps > 0) {
+    if (in_tile < n_tiles && steps > 0) {
       const uint32_t stage = ring0 + in_stage, codes = stage + my_codes;
       const int c = in_c;
       const int left = (int)row_words - c * (8 * BITS);  // words of a row from here on
       if (BITS == 4 || a.wide_rows) {
-        if (left >= 8 * BITS) {
 #pragma unroll
-          for (int i = 0; i < PP; ++i) copy_async<16>(codes + piece_dst(lane + 32 * i), words + piece_src(lane + 32 * i));
-        } else {
-#pragma unroll
-          for (int i = 0; i < PP; ++i) {
-            const int p = lane + 32 * i;
-            const bool ok = p % PP * 4 < left;
-            copy_async<16>(codes + piece_dst(p), ok ? words + piece_src(p) : words, ok);
-          }
+        for (int i = 0; i < NI; ++i) {
+          const bool ok = left >= 8 * BITS || (lane + 32 * i) % PP * 4 < left;
+          copy_async<16>(codes + dst_of[i], words0 + (ok ? src_of[i] : 0), ok);
+          copy_async<16>(codes + 16 * RS + dst_of[i], words1 + (ok ? src_of[i] : 0), ok);
         }
-      } else {  // rows on any 4 bytes: word by word
+      } else {  // rows on any 4 bytes: row `lane`, word by word
+        const uint32_t* src = (lane < 16 ? words0 : words1) + (lane & 15) * row_words;
 #pragma unroll 1
-        for (int p = lane; p < 32 * PP * 4; p += 32) {
-          const bool ok = (p / 4) % PP * 4 + p % 4 < left;
-          copy_async<4>(codes + piece_dst(p / 4) + p % 4 * 4, ok ? words + piece_src(p / 4) + p % 4 : words, ok);
+        for (int p = 0; p < 8 * BITS; ++p) {
+          const bool ok = p < left;
+          copy_async<4>(codes + lane * RS + ((p >> 2) ^ (half_bit<BITS>(lane) * BITS)) * 16 + (p & 3) * 4, ok ? src + p : src, ok);
         }
       }
       const uint32_t grids = codes + 32 * RS + lane * (2 * SUB * 4);  // [row][chunk, quarter] scales, then zeros
@@ -618,12 +620,12 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
         }
       }
       in_c += a.k_warps;
-      words += a.k_warps * (8 * BITS);
+      words0 += a.k_warps * (8 * BITS), words1 += a.k_warps * (8 * BITS);
       token_src += a.k_warps * 256;
       stat_src += a.k_warps * 2;
       if (in_c >= a.spans) {
         in_c = kw;
-        in_item += gridDim.x;
+        hop(in_tile, in_rt);
         begin_item();
       }
     }
@@ -636,17 +638,22 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
   for (int s = 0; s < kStages - 1; ++s) issue();
 
   uint32_t out_stage = 0;
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const int first = a.lists->tiles[item / per_tile].first, count = a.lists->tiles[item / per_tile].count;
-    // Columns past the tile's last token repeat it (nobody reads them).  This lane's column of B is entry g of every
-    // 8 (quad 0's piece; quad q's is that with q exchanged into its place), its columns of the sums are
-    // entries 2 t and 2 t + 1.
-    int tok[NT], col[NT][2];
+  int at_tile = -1, first = 0, count = 0;
+  int tok[NT], col[NT][2];
+  int tile = (int)blockIdx.x / per_tile, rt0 = (int)blockIdx.x % per_tile;
+  for (; tile < n_tiles; hop(tile, rt0)) {
+    if (tile != at_tile) {
+      at_tile = tile;
+      first = a.lists->tiles[tile].first, count = a.lists->tiles[tile].count;
+      // Columns past the tile's last token repeat it (nobody reads them).  This lane's column of B is entry g of every
+      // 8 (quad 0's piece; quad q's is that with q exchanged into its place), its columns of the sums are
+      // entries 2 t and 2 t + 1.
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int j = min(8 * n + g, count - 1);
-      tok[n] = j * (TERMS * 512) + ((t ^ 4 * (j & 1)) << 4);
-      col[n][0] = min(8 * n + 2 * t, count - 1), col[n][1] = min(8 * n + 2 * t + 1, count - 1);
+      for (int n = 0; n < NT; ++n) {
+        const int j = min(8 * n + g, count - 1);
+        tok[n] = j * (TERMS * 512) + ((t ^ 4 * (j & 1)) << 4);
+        col[n][0] = min(8 * n + 2 * t, count - 1), col[n][1] = min(8 * n + 2 * t + 1, count - 1);
+      }
     }
     float acc[2][NT][4];
 #pragma unroll
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
       const uint8_t* stage = ring + out_stage;
       out_stage += stage_bytes;
       if (out_stage == ring_end) out_stage = 0;
-#pragma unroll 1
+#pragma unroll
       for (int h = 0; h < 2; ++h) {  // the span's chunks
         const uint8_t* codes = stage + my_codes;
         uint32_t w[4][BITS];
@@ -768,9 +775,10 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
         lo[0] = acc[m][n][0], lo[1] = acc[m][n][1], hi[0] = acc[m][n][2], hi[1] = acc[m][n][3];
       }
     __syncthreads();
-    for (int i = threadIdx.x; i < groups * tile_rows * count; i += kProductWarps * 32) {
-      const int r = i % tile_rows, j = i / tile_rows % groups, n = i / (tile_rows * groups);
-      const int rt = item % per_tile * groups + j;
+    const int out_rows = groups * tile_rows;  // powers of two
+    for (int i = threadIdx.x; i < out_rows * count; i += kProductWarps * 32) {
+      const int r = i & (tile_rows - 1), j = (i & (out_rows - 1)) >> (gated ? 4 : 5), n = i >> (31 - __clz(out_rows));
+      const int rt = rt0 * groups + j;
       if (rt >= a.row_tiles) continue;
       float v = 0.0f, up = 0.0f;
       for (int w = j; w < kProductWarps; w += groups) {
