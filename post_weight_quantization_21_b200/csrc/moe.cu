@@ -116,6 +116,26 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// ------------------------------------------------------------------ chained launches
+// All launches but the first may start while the one before still runs (programmatic dependent launch): their
+// threads wait here, before they touch memory, until it has ended and its writes are visible.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ------------------------------------------------------------------ workspace
 struct Tile {  // up to 8 NT tokens of one expert: entries [first, first + count) of the pair list
   int32_t expert, first, count;
@@ -255,6 +275,7 @@ template <typename T, int BITS, int TERMS>
 __global__ void __launch_bounds__(256) moe_router_kernel(const T* __restrict__ X, const T* __restrict__ R, int tokens,
                                                          int d, int experts, int router_blocks,
                                                          float* __restrict__ logits, const Terms terms) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if ((int)blockIdx.x < router_blocks) {
     const int e = blockIdx.x % experts, t0 = blockIdx.x / experts * kRouterTokens;
     const int nt = min(kRouterTokens, tokens - t0);
@@ -301,6 +322,7 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const T* __restrict__ X
 template <int BITS, int TERMS>
 __global__ void __launch_bounds__(256) moe_layout_kernel(const float* __restrict__ acts, int64_t rows, int cols,
                                                          const Terms terms) {
+  wait_for_previous();
   const int per_row = terms.chunks * 4;
   const int64_t n = rows * per_row;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -323,6 +345,7 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict
                                                          Lists* __restrict__ lists, int32_t* status) {
   __shared__ int32_t id_of[kMaxPairs];
   __shared__ int32_t first_of[kMaxExperts], tile_of[kMaxExperts];
+  wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = tokens * top_k;
   if (logits != nullptr) {
@@ -504,6 +527,7 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
   const bool gated = a.mode == kUpGated;
   const int tile_rows = gated ? 16 : 32;
   const int64_t row_words = (int64_t)a.units * BITS;
+  wait_for_previous();
   if ((int)blockIdx.x >= a.lists->n_tiles * per_tile) return;
   for (int i = threadIdx.x; i < a.pairs; i += kProductWarps * 32) {
     const int p = a.lists->pairs[i];
@@ -811,6 +835,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const float* __restric
                                                           const int32_t* __restrict__ ids,
                                                           const float* __restrict__ weights, int tokens, int d,
                                                           int top_k, int experts, TY* __restrict__ Y) {
+  wait_for_previous();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)tokens * d) return;
   const int t = (int)(i / d), c = (int)(i % d);
@@ -836,7 +861,9 @@ int choose_k_warps(const ProductArgs& a, int tiles, int slots, int* smem) {
     const int bytes = kStages * (kProductWarps * warp_stage_bytes<BITS, SUB>() + kw * token_stage_bytes(a.cols, TERMS, SUB));
     const int groups = kProductWarps / kw;
     const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
-    const int64_t cost = (items + slots - 1) / slots * ((a.spans + kw - 1) / kw + 1);
+    // few groups read short runs of many rows at once, and DRAM answers more slowly: one token on 4096 x 11008
+    // experts took 52, 53, 88 and 122 us with 8, 4, 2 and 1
+    const int64_t cost = (items + slots - 1) / slots * ((a.spans + kw - 1) / kw + 1) * (kw >= 4 ? 8 : (kw == 2 ? 13 : 18));
     if (best_cost == INT64_MAX ? bytes <= kRoom || kw == 1 : bytes <= kRoom && cost < best_cost)
       best = kw, best_cost = cost, *smem = bytes;
   }
@@ -856,7 +883,7 @@ gptq_status launch_product_form(ProductArgs a, int tiles, int sms, cudaStream_t 
   const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
   auto kernel = moe_product_kernel<BITS, TERMS, NT, SUB>;
   GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  kernel<<<(int)std::min<int64_t>(items, slots), kProductWarps * 32, smem, s>>>(a);
+  GPTQ_CUDA_TRY(launch_chained(kernel, (unsigned)std::min<int64_t>(items, slots), kProductWarps * 32, smem, s, a));
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -901,14 +928,16 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
     default: st = launch_router<float, BITS, 2>(m, logits, x_terms, s); break;
   }
   if (st != GPTQ_OK) return st;
-  // up to 8 tokens an expert's list is one N tile; longer lists go 16 at a time so that the codes are taken
-  // apart once for two N tiles (scales that change inside a chunk need the registers: 8 at a time)
+  // An expert's list goes 8 tokens at a time, or 16 where lists are long (more than 12 on average), so that the
+  // codes are taken apart once for two N tiles; 16 tokens' terms leave fewer groups room, so for short lists they
+  // only cost (32 tokens, 6 of 32 experts each: 196 us with 16 at a time, 152 with 8).  Scales that change inside
+  // a chunk need the registers of the second N tile.
   const bool sub = m.group_size == 32 || m.group_size == 64;
-  const int nt = tokens <= 8 || sub ? 1 : 2;
+  const int nt = pairs <= 12 * m.experts || sub ? 1 : 2;
   const int tile_tokens = 8 * nt;
   const int tiles = std::min(pairs, std::min(m.experts, pairs) + pairs / tile_tokens);  // at most
-  moe_route_kernel<<<1, 1024, 0, s>>>(m.router ? logits : nullptr, tokens, m.experts, m.top_k, m.renormalize,
-                                      tile_tokens, m.ids, m.weights, lists, m.status);
+  GPTQ_CUDA_TRY(launch_chained(moe_route_kernel, 1, 1024, 0, s, m.router ? logits : nullptr, tokens, m.experts, m.top_k,
+                               m.renormalize, tile_tokens, m.ids, m.weights, lists, m.status));
   GPTQ_LAUNCH_CHECK();
   ProductArgs a = {};
   a.mode = m.gated ? kUpGated : kUpRelu;
@@ -930,9 +959,9 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   if (st != GPTQ_OK) return st;
   const unsigned layout_blocks = (unsigned)(((int64_t)pairs * a_terms.chunks * 4 + 255) / 256);
   if (a_wide)
-    moe_layout_kernel<BITS, 2><<<layout_blocks, 256, 0, s>>>(acts, pairs, f, a_terms);
+    GPTQ_CUDA_TRY(launch_chained(moe_layout_kernel<BITS, 2>, layout_blocks, 256, 0, s, acts, pairs, f, a_terms));
   else
-    moe_layout_kernel<BITS, 1><<<layout_blocks, 256, 0, s>>>(acts, pairs, f, a_terms);
+    GPTQ_CUDA_TRY(launch_chained(moe_layout_kernel<BITS, 1>, layout_blocks, 256, 0, s, acts, pairs, f, a_terms));
   GPTQ_LAUNCH_CHECK();
   a.mode = kDown;
   a.a = matrix(m.down);
@@ -946,9 +975,9 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   if (st != GPTQ_OK) return st;
   const unsigned blocks = (unsigned)(((int64_t)tokens * d + 255) / 256);
   switch (m.y_dtype) {
-    case GPTQ_BF16: moe_combine_kernel<<<blocks, 256, 0, s>>>(products, m.ids, m.weights, tokens, d, m.top_k, m.experts, static_cast<__nv_bfloat16*>(m.Y)); break;
-    case GPTQ_FP16: moe_combine_kernel<<<blocks, 256, 0, s>>>(products, m.ids, m.weights, tokens, d, m.top_k, m.experts, static_cast<__half*>(m.Y)); break;
-    default: moe_combine_kernel<<<blocks, 256, 0, s>>>(products, m.ids, m.weights, tokens, d, m.top_k, m.experts, static_cast<float*>(m.Y)); break;
+    case GPTQ_BF16: GPTQ_CUDA_TRY(launch_chained(moe_combine_kernel<__nv_bfloat16>, blocks, 256, 0, s, products, m.ids, m.weights, tokens, d, m.top_k, m.experts, static_cast<__nv_bfloat16*>(m.Y))); break;
+    case GPTQ_FP16: GPTQ_CUDA_TRY(launch_chained(moe_combine_kernel<__half>, blocks, 256, 0, s, products, m.ids, m.weights, tokens, d, m.top_k, m.experts, static_cast<__half*>(m.Y))); break;
+    default: GPTQ_CUDA_TRY(launch_chained(moe_combine_kernel<float>, blocks, 256, 0, s, products, m.ids, m.weights, tokens, d, m.top_k, m.experts, static_cast<float*>(m.Y))); break;
   }
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
