@@ -294,21 +294,33 @@ def gptq_dequantize(packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Ten
 
 
 # ------------------------------------------------------------------------------------------ fp8 operands
-def _shaped(t: torch.Tensor, name: str, shape: tuple, dtype, dev):
-    """A contiguous tensor of this shape and type (one type or a mapping of types) on ``dev``."""
-    if t.shape != shape or not (t.dtype in dtype if isinstance(dtype, dict) else t.dtype == dtype):
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} "
-                         f"{' / '.join(map(str, dtype)) if isinstance(dtype, dict) else dtype}")
-    if t.device != dev or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+_ANY_FLOAT = tuple(_DTYPES)
+_F8, _F32, _I32 = (torch.float8_e4m3fn,), (torch.float32,), (torch.int32,)
 
 
-def _on(dev: torch.device, stream, call):
-    """``call(stream)`` with ``dev`` current: the library launches on the current device."""
-    if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
+def _shaped(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, dev: int):
+    """Refuses anything but a contiguous tensor of this shape and of one of these types on CUDA device ``dev``."""
+    if t.shape != shape or t.dtype not in dtypes:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {' / '.join(map(str, dtypes))}")
+    if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor, on device {dev} like the others")
+
+
+def _work(t: torch.Tensor, dev: int) -> int:
+    """Bytes of a workspace."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on device {dev}")
+    return t.numel() * t.element_size()
+
+
+def _on(dev: int, stream, call):
+    """``call(stream)`` with ``dev`` current (the library launches on the current device), by default on the stream
+    current on that device."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == dev:
+        return call(s)
     with torch.cuda.device(dev):
-        return call(_stream(stream))
+        return call(s)
 
 
 def gptq_fp8_quantize(X: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, stream=None):
@@ -317,12 +329,12 @@ def gptq_fp8_quantize(X: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor, bl
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows {block_rows}: 1 or 128")
     m, k = X.shape
-    dev = X.device
-    _shaped(X, "X", (m, k), _DTYPES, dev)
-    _shaped(Q, "Q", (m, k), torch.float8_e4m3fn, dev)
-    _shaped(scales, "scales", (-(-m // block_rows), -(-k // 128)), torch.float32, dev)
-    st = _on(dev, stream, lambda s: lib().gptq_fp8_quantize(_ptr(X), _DTYPES[X.dtype], m, k, block_rows, _ptr(Q),
-                                                             _ptr(scales), s))
+    dev = X.get_device()
+    _shaped(X, "X", (m, k), _ANY_FLOAT, dev)
+    _shaped(Q, "Q", (m, k), _F8, dev)
+    _shaped(scales, "scales", (-(-m // block_rows), -(-k // 128)), _F32, dev)
+    st = _on(dev, stream, lambda s: lib().gptq_fp8_quantize(X.data_ptr(), _DTYPES[X.dtype], m, k, block_rows, Q.data_ptr(),
+                                                             scales.data_ptr(), s))
     _check(st, "gptq_fp8_quantize")
 
 
@@ -331,15 +343,15 @@ def gptq_fp8_from_packed(packed: torch.Tensor, scales: torch.Tensor, zeros: torc
     """A quantized layer as e4m3 operands, without rounding: Q [m, k] = q - zero and q_scales [m, ceil(k / 128)] the
     grids' scales (group_size 0 or a multiple of 128)."""
     m, k = Q.shape
-    dev = Q.device
+    dev = Q.get_device()
     ng = k // group_size if group_size > 0 else 1
-    _shaped(Q, "Q", (m, k), torch.float8_e4m3fn, dev)
-    _shaped(packed, "packed", (m, k * bits // 32), torch.int32, dev)
-    _shaped(scales, "scales", (m, ng), torch.float32, dev)
-    _shaped(zeros, "zeros", (m, ng), torch.int32, dev)
-    _shaped(q_scales, "q_scales", (m, -(-k // 128)), torch.float32, dev)
-    st = _on(dev, stream, lambda s: lib().gptq_fp8_from_packed(_ptr(packed), _ptr(scales), _ptr(zeros), m, k, bits,
-                                                                group_size, _ptr(Q), _ptr(q_scales), s))
+    _shaped(Q, "Q", (m, k), _F8, dev)
+    _shaped(packed, "packed", (m, k * bits // 32), _I32, dev)
+    _shaped(scales, "scales", (m, ng), _F32, dev)
+    _shaped(zeros, "zeros", (m, ng), _I32, dev)
+    _shaped(q_scales, "q_scales", (m, -(-k // 128)), _F32, dev)
+    st = _on(dev, stream, lambda s: lib().gptq_fp8_from_packed(packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), m, k, bits,
+                                                                group_size, Q.data_ptr(), q_scales.data_ptr(), s))
     _check(st, "gptq_fp8_from_packed")
 
 
@@ -355,18 +367,17 @@ def gptq_fp8_matmul(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_
         raise ValueError(f"b_block_rows {b_block_rows}: 1 or 128")
     m, k = A.shape
     n = B.shape[0]
-    kb, dev = -(-k // 128), A.device
-    _shaped(A, "A", (m, k), torch.float8_e4m3fn, dev)
-    _shaped(B, "B", (n, k), torch.float8_e4m3fn, dev)
-    _shaped(a_scales, "a_scales", (m, kb), torch.float32, dev)
-    _shaped(b_scales, "b_scales", (-(-n // b_block_rows), kb), torch.float32, dev)
-    _shaped(Y, "Y", (m, n), _DTYPES, dev)
-    _shaped(status, "status", (2,), torch.int32, dev)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    kb, dev = -(-k // 128), A.get_device()
+    _shaped(A, "A", (m, k), _F8, dev)
+    _shaped(B, "B", (n, k), _F8, dev)
+    _shaped(a_scales, "a_scales", (m, kb), _F32, dev)
+    _shaped(b_scales, "b_scales", (-(-n // b_block_rows), kb), _F32, dev)
+    _shaped(Y, "Y", (m, n), _ANY_FLOAT, dev)
+    _shaped(status, "status", (2,), _I32, dev)
+    ws = _work(workspace, dev)
     st = _on(dev, stream, lambda s: lib().gptq_fp8_matmul(
-        _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), b_block_rows, m, n, k, _ptr(Y), _DTYPES[Y.dtype],
-        _ptr(status), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+        A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(), b_block_rows, m, n, k, Y.data_ptr(), _DTYPES[Y.dtype],
+        status.data_ptr(), workspace.data_ptr(), ws, s))
     _check(st, "gptq_fp8_matmul")
 
 
@@ -385,7 +396,7 @@ def gptq_moe_layer(X: torch.Tensor, router: torch.Tensor | None, up: tuple, gate
     [n_experts, f, d*bits/32] for up and gate, [n_experts, d, f*bits/32] for down.  ``router`` [n_experts, d] in X's
     type fills topk_ids and topk_weights [tokens, top_k]; without one they are the routing to use."""
     tokens, d = X.shape
-    dev, dt = X.device, X.dtype
+    dev, dt = X.get_device(), X.dtype
     top_k = topk_ids.shape[1]
     if bits not in (2, 3, 4) or group_size < 0:
         raise ValueError(f"bits {bits}, group_size {group_size}")
@@ -393,27 +404,26 @@ def gptq_moe_layer(X: torch.Tensor, router: torch.Tensor | None, up: tuple, gate
 
     def matrices(w, name, rows, cols):
         ng = cols // group_size if group_size else 1
-        _shaped(w[0], name + " packed", (experts, rows, cols * bits // 32), torch.int32, dev)
-        _shaped(w[1], name + " scales", (experts, rows, ng), torch.float32, dev)
-        _shaped(w[2], name + " zeros", (experts, rows, ng), torch.int32, dev)
+        _shaped(w[0], name + " packed", (experts, rows, cols * bits // 32), _I32, dev)
+        _shaped(w[1], name + " scales", (experts, rows, ng), _F32, dev)
+        _shaped(w[2], name + " zeros", (experts, rows, ng), _I32, dev)
         return MoeWeights(*(t.data_ptr() for t in w))
 
-    _shaped(X, "X", (tokens, d), _DTYPES, dev)
+    _shaped(X, "X", (tokens, d), _ANY_FLOAT, dev)
     if router is not None:
-        _shaped(router, "router", (experts, d), dt, dev)
-    _shaped(topk_ids, "topk_ids", (tokens, top_k), torch.int32, dev)
-    _shaped(topk_weights, "topk_weights", (tokens, top_k), torch.float32, dev)
-    _shaped(Y, "Y", (tokens, d), _DTYPES, dev)
-    _shaped(status, "status", (2,), torch.int32, dev)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+        _shaped(router, "router", (experts, d), (dt,), dev)
+    _shaped(topk_ids, "topk_ids", (tokens, top_k), _I32, dev)
+    _shaped(topk_weights, "topk_weights", (tokens, top_k), _F32, dev)
+    _shaped(Y, "Y", (tokens, d), _ANY_FLOAT, dev)
+    _shaped(status, "status", (2,), _I32, dev)
+    ws = _work(workspace, dev)
     u, w = matrices(up, "up", f, d), matrices(down, "down", d, f)
     g = None if gate is None else matrices(gate, "gate", f, d)
     c = MoeCfg(experts, top_k, bits, group_size, activation, flags)
     st = _on(dev, stream, lambda s: lib().gptq_moe_layer(
-        _ptr(X), _DTYPES[dt], tokens, d, f, ctypes.byref(c), _ptr(router), ctypes.byref(u),
-        None if g is None else ctypes.byref(g), ctypes.byref(w), _ptr(topk_ids), _ptr(topk_weights), _ptr(Y),
-        _DTYPES[Y.dtype], _ptr(status), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+        X.data_ptr(), _DTYPES[dt], tokens, d, f, ctypes.byref(c), _ptr(router), ctypes.byref(u),
+        None if g is None else ctypes.byref(g), ctypes.byref(w), topk_ids.data_ptr(), topk_weights.data_ptr(), Y.data_ptr(),
+        _DTYPES[Y.dtype], status.data_ptr(), workspace.data_ptr(), ws, s))
     _check(st, "gptq_moe_layer")
 
 
