@@ -30,7 +30,7 @@ using namespace tc;
 
 constexpr int BM = 128;           // tokens per tile
 constexpr int BK = 128;           // columns per block (and per stage): 128 bytes, one swizzle row
-constexpr int SG = 8;             // blocks whose token scales are staged at a time
+constexpr int SG = 4;             // blocks whose token scales are staged at a time
 constexpr int kPlanSMs = 148;
 constexpr int kGroupTiles = 16;   // token tiles walked together (see unit_coords)
 constexpr int kSmemBudget = 200 * 1024;
@@ -45,7 +45,7 @@ struct Cfg {
   static constexpr int kAccs = 4;  // accumulators in TMEM
   static constexpr int kTmemCols = NT * kAccs < 32 ? 32 : NT * kAccs;
   static constexpr int kCols = NT * 4 / kEpiWarps;  // weight rows per epilogue warp
-  static constexpr int kScaleRow = 2 * BM > BM + NT ? 2 * BM : BM + NT;  // staged scales per block
+  static constexpr int kScaleRow = BM + NT;  // staged scales per block
   static constexpr int kScaleBytes = 2 * SG * kScaleRow * 4;
   static constexpr int kSmem = kStages * kStageBytes + kScaleBytes + 1024 + 512;
 };
@@ -54,7 +54,8 @@ struct Args {
   int m, n, kb;                    // tokens, weight rows, blocks
   int tiles_t, tiles_w, units;     // token tiles, weight tiles, work units
   int kb_per_split;
-  bool vec_scales, vec_y;          // 16-byte accesses to the scales' and Y's rows are aligned
+  int scale_width;                 // floats per load that the scales' rows are aligned for: 1, 2 or 4
+  bool vec_y;                      // 16-byte accesses to Y's rows are aligned
   int token_bytes;                 // bytes of a stage's token box (fewer than 128 rows when m is small)
   uint32_t idesc;
   const float* a_scales;
@@ -62,6 +63,25 @@ struct Args {
   void* Y;
   float* partial;                  // [split][m][n] when the blocks are split, else null
   int32_t* status;
+};
+
+// One lane of a converged warp.  The producer's and the issuers' loops run in whole warps with only the TMA, MMA and
+// commit instructions under this predicate: their operands then stay in the warp's uniform registers.  With the
+// loops inside `if (lane == 0)` every operand was moved there first, and a block's four MMAs and two commits
+// took their thread 730 cycles, more than the tensor core needs for them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// position in a ring of N slots: the slot, and the parity of the round
+template <int N>
+struct Ring {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, parity ^= 1;
+  }
 };
 
 __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -78,6 +98,15 @@ __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_
 // r[4 j + {2, 3}] the same columns of row lane / 4 + 8; there after tmem_wait()
 template <int J>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 template <>
 __device__ __forceinline__ void tmem_ld<2>(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -157,24 +186,30 @@ __device__ __forceinline__ void store_row(const uint64_t (&acc)[NC / 2], T* y, i
   }
 }
 
-// scales of blocks g0 .. g0 + N - 1 of one row (zero past the last block b1); vec: rows start on 16 bytes and
-// g0 is a multiple of 4.  One row's scales are kb floats away from the next row's, so every lane reads a
-// line of its own: two 16-byte loads take a quarter of eight 4-byte loads' time in the load unit.
-template <int N>
-__device__ __forceinline__ void fetch_scales(const float* p, int g0, int b1, bool vec, float (&v)[N]) {
-  if (vec) {
+// Scales of blocks g0 .. g0 + 3 of one row of kb (past its end: some of its others, which nobody uses), V at a time:
+// rows start on 4 V bytes, g0 is a multiple of 4.  One row's scales are kb floats away from the next row's, so every
+// lane reads a line of its own: one 16-byte load takes a quarter of four 4-byte loads' time in the load unit.
+// The loads are volatile and without conditions so that they stay where they are written, a group of blocks before
+// their use, and go straight into the registers that are used: moved down by the compiler, or merged with
+// zeros behind a condition, they cost their latency, some 700 cycles a group.
+template <int V>
+__device__ __forceinline__ void fetch_scales(const float* row, int g0, int kb, float (&v)[4]) {
+  if constexpr (V == 4) {
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "l"(row + min(g0, kb - 4)));
+  } else if constexpr (V == 2) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 f = g0 + i < b1 ? __ldg(reinterpret_cast<const float4*>(p + g0 + i)) : make_float4(0, 0, 0, 0);
-      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
-    }
+    for (int i = 0; i < 4; i += 2)
+      asm volatile("ld.global.nc.v2.f32 {%0, %1}, [%2];" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(row + min(g0 + i, kb - 2)));
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = g0 + i < b1 ? __ldg(p + g0 + i) : 0.0f;
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v[i]) : "l"(row + min(g0 + i, kb - 1)));
   }
 }
 
-template <int NT, bool BLOCK, typename TY>
+template <int NT, bool BLOCK, int VEC, typename TY>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
                       const Args a) {
@@ -190,7 +225,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -200,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], C::kEpiWarps);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -212,76 +247,75 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      uint32_t stage = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-        int tt, tw, s;
-        unit_coords(u, a, tt, tw, s);
-        const int b0 = s * a.kb_per_split, b1 = min(a.kb, b0 + a.kb_per_split);
-        for (int b = b0; b < b1; ++b, ++stage) {
-          const uint32_t slot = stage % C::kStages, round = stage / C::kStages;
-          if (!mbar_wait(&empty[slot], (round & 1) ^ 1, abort_flag, a.status, 51)) {
-            ok = false;
-            break;
-          }
-          uint8_t* T = smem + slot * C::kStageBytes;
-          mbar_expect_tx(&full[slot], (uint32_t)a.token_bytes + NT * BK);
-          tma_load_2d(T, &map_t, b * BK, tt * BM, &full[slot]);
-          tma_load_2d(T + BM * BK, &map_w, b * BK, tw * NT, &full[slot]);
+    Ring<C::kStages> r;
+    uint32_t issued = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+      int tt, tw, s;
+      unit_coords(u, a, tt, tw, s);
+      const int b0 = s * a.kb_per_split, b1 = min(a.kb, b0 + a.kb_per_split);
+      for (int b = b0; b < b1; ++b, ++issued, r.next()) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[r.slot], r.parity ^ 1, abort_flag, a.status, 51));
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* T = smem + r.slot * C::kStageBytes;
+          mbar_expect_tx(&full[r.slot], (uint32_t)a.token_bytes + NT * BK);
+          tma_load_2d(T, &map_t, b * BK, tt * BM, &full[r.slot]);
+          tma_load_2d(T + BM * BK, &map_w, b * BK, tw * NT, &full[r.slot]);
         }
-      }
-      if (!ok) {  // let the copies already issued land before the CTA leaves
-        const uint32_t first = stage > C::kStages ? stage - C::kStages : 0;
-        for (uint32_t i = first; i < stage; ++i) mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1);
+        __syncwarp();
       }
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      uint32_t stage = 0;  // blocks issued so far: stage slot and accumulator follow from it
-      bool ok = true;
-      const uint32_t smem0 = smem_u32(smem);
-      for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-        int tt, tw, s;
-        unit_coords(u, a, tt, tw, s);
-        const int nb = min(a.kb, (s + 1) * a.kb_per_split) - s * a.kb_per_split;
-        for (int b = 0; b < nb; ++b, ++stage) {
-          const uint32_t buf = stage % C::kAccs, use = stage / C::kAccs;
-          const uint32_t slot = stage % C::kStages, round = stage / C::kStages;
-          if (!mbar_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, a.status, 52) ||
-              !mbar_wait(&full[slot], round & 1, abort_flag, a.status, 53)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // K-major rows of 128 bytes with the 128-byte swizzle; a step of 32 columns is 32 bytes.  Token rows
-          // that the box does not reach hold what was there before: they only reach accumulator rows
-          // that nobody reads.
-          const uint64_t td = sdesc_sw128(smem0 + slot * C::kStageBytes, 16, 1024);
-          const uint64_t wd = sdesc_sw128(smem0 + slot * C::kStageBytes + BM * BK, 16, 1024);
+    if (!ok) {  // let the copies already issued land before the CTA leaves
+      const uint32_t first = issued > C::kStages ? issued - C::kStages : 0;
+      for (uint32_t i = first; i < issued; ++i) mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1);
+    }
+  } else if (warp < 3) {
+    // ---------------------------------------------------------------- MMA issuers: even and odd blocks
+    Ring<C::kStages> r;
+    Ring<C::kAccs> acc;
+    uint32_t mine = warp - 1;  // 0: this block is this warp's
+    bool ok = true;
+    const uint64_t desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+    for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+      int tt, tw, s;
+      unit_coords(u, a, tt, tw, s);
+      const int nb = min(a.kb, (s + 1) * a.kb_per_split) - s * a.kb_per_split;
+      for (int b = 0; b < nb; ++b, r.next(), acc.next(), mine ^= 1) {
+        if (mine) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[acc.slot], acc.parity ^ 1, abort_flag, a.status, 52) &&
+                                         mbar_wait(&full[r.slot], r.parity, abort_flag, a.status, 53));
+        if (!ok) break;
+        tc_fence_after();
+        // K-major rows of 128 bytes with the 128-byte swizzle; a step of 32 columns is 32 bytes.  Token rows
+        // that the box does not reach hold what was there before: they only reach accumulator rows
+        // that nobody reads.
+        if (elect_one()) {
+          const uint64_t td = desc0 + (uint64_t)((r.slot * C::kStageBytes) >> 4);
+          const uint64_t wd = td + (uint64_t)((BM * BK) >> 4);
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            umma_f8(tmem_base + buf * NT, td + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), a.idesc, kk > 0 ? 1u : 0u);
-          umma_commit(&empty[slot]);
-          umma_commit(&acc_full[buf]);
+            umma_f8(tmem_base + acc.slot * NT, td + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), a.idesc, kk > 0 ? 1u : 0u);
+          umma_commit(&acc_full[acc.slot]);
+          umma_commit(&empty[r.slot]);
         }
+        __syncwarp();
       }
-      // all MMAs issued by this thread are complete before TMEM is released
-      umma_commit(drain);
-      mbar_wait_drain(drain, 0);
     }
+    // all MMAs issued by this warp are complete before TMEM is released
+    if (elect_one()) umma_commit(drain);
     __syncwarp();
+    mbar_wait_drain(drain, 0);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int quad = warp & 3;         // TMEM lanes this warp may access: 32*quad .. 32*quad+31
     const int part = (warp - 4) >> 2;  // columns kCols * part .. of the tile
     const int et = threadIdx.x - 128;
     const int r4 = lane >> 2, c4 = 2 * (lane & 3);  // this thread's rows r4 + 8 i and columns c4 + 8 j + {0, 1}
-    constexpr int J = 2;       // 8-column groups per load
-    constexpr int NQ = C::kCols / (8 * J);
+    constexpr int J = C::kCols < 32 ? 2 : 4, NQ = C::kCols / (8 * J);  // 8-column groups per load, loads per block
     constexpr int SR = C::kScaleRow;
-    uint32_t stage = 0, group = 0;
+    uint32_t group = 0;
+    Ring<C::kAccs> at;  // the accumulator of the block in hand
     // After a wait that gave up the warp stops waiting and storing but still walks its units, because all
     // eight warps have to meet at the named barrier.
     bool ok = true;
@@ -290,16 +324,16 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
       unit_coords(u, a, tt, tw, s);
       const int b0 = s * a.kb_per_split, b1 = min(a.kb, b0 + a.kb_per_split);
       const int t0 = tt * BM, w0 = tw * NT;
-      // Scales are staged SG blocks at a time, one row and one column per thread.  BLOCK: the scale of the
-      // warp half's weight rows (they lie in one block of 128) times the token's; else the two apart.
-      const int st_half = et >> 7 & 1;
-      const float* tsc = a.a_scales + (int64_t)min(t0 + (et & 127), a.m - 1) * a.kb;
-      const float* wsc = BLOCK ? a.b_scales + (int64_t)(min(w0 + st_half * 128, a.n - 1) >> 7) * a.kb
-                               : a.b_scales + (int64_t)min(w0 + et, a.n - 1) * a.kb;
+      // Scales are staged SG blocks at a time: the first half of the threads the tokens', the second half the weight
+      // rows'.  BLOCK: the first half both, multiplied (the tile's weight rows lie in one block of 128).
+      const int row = et & 127;
+      const float* tsc = a.a_scales + (int64_t)min(t0 + row, a.m - 1) * a.kb;
+      const float* wsc = BLOCK ? a.b_scales + (int64_t)(w0 >> 7) * a.kb
+                               : a.b_scales + (int64_t)min(w0 + min(row, NT - 1), a.n - 1) * a.kb;
       float t_next[SG], w_next[SG];  // the scales of the group to come
       auto fetch = [&](int g0) {
-        if (BLOCK ? et < 2 * BM : et < BM) fetch_scales<SG>(tsc, g0, b1, a.vec_scales, t_next);
-        if (BLOCK ? et < 2 * BM : et < NT) fetch_scales<SG>(wsc, g0, b1, a.vec_scales, w_next);
+        if (part == 0) fetch_scales<VEC>(tsc, g0, a.kb, t_next);
+        if (BLOCK ? part == 0 : part == 1) fetch_scales<VEC>(wsc, g0, a.kb, w_next);
       };
       fetch(b0);
       const bool rows_here = t0 + 32 * quad < a.m;  // else the warp only keeps the barriers going
@@ -312,57 +346,48 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
         float* sc = token_scales + (group & 1) * SG * SR;  // the other buffer may still be read
 #pragma unroll
         for (int i = 0; i < SG; ++i) {
-          if (BLOCK) {
-            if (et < 2 * BM) sc[i * SR + et] = t_next[i] * w_next[i];  // [block of weight rows][token]
-          } else {
-            if (et < BM) sc[i * SR + et] = t_next[i];  // [token], then [weight row]
-            if (et < NT) sc[i * SR + BM + et] = w_next[i];
-          }
+          if (part == 0) sc[i * SR + row] = BLOCK ? t_next[i] * w_next[i] : t_next[i];  // [token], then [weight row]
+          if (!BLOCK && part == 1 && row < NT) sc[i * SR + BM + row] = w_next[i];
         }
         fetch(g0 + SG);
         asm volatile("bar.sync 1, %0;" ::"n"(C::kEpiThreads) : "memory");
         const int g1 = min(b1, g0 + SG);
-        const float* rsc = sc + (BLOCK ? (part * C::kCols >> 7) * BM : 0) + 32 * quad + r4;
+        const float* rsc = sc + 32 * quad + r4;
         const float* csc = sc + BM + part * C::kCols + c4;
-        for (int b = g0; b < g1; ++b, ++stage, rsc += SR, csc += SR) {
-          const uint32_t buf = stage % C::kAccs, use = stage / C::kAccs;
+        for (int b = g0; b < g1; ++b, rsc += SR, csc += SR) {
           uint64_t rs[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t v = __float_as_uint(rsc[8 * i]);
-            rs[i] = pack2(v, v);
+            const uint32_t r = __float_as_uint(rsc[8 * i]);
+            rs[i] = pack2(r, r);
           }
-          if (ok) ok = mbar_wait(&acc_full[buf], use & 1, abort_flag, a.status, 54);
+          if (ok) ok = mbar_wait(&acc_full[at.slot], at.parity, abort_flag, a.status, 54);
           tc_fence_after();
-          const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * NT + part * C::kCols;
-          if (!rows_here) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
-            continue;
-          }
-          // the next columns are on their way from TMEM while these are added
-          uint32_t v[2][2][4 * J];  // [buffer][16-row half]
-          tmem_ld<J>(taddr, v[0][0]);
-          tmem_ld<J>(taddr + (16u << 16), v[0][1]);
+          // Two loads a block, waited for one by one: running them ahead of the sums, across blocks, took longer (a
+          // block of 128 x 128 1000 cycles instead of 700).
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            tmem_wait();
-            if (q + 1 < NQ) {
-              tmem_ld<J>(taddr + 8 * J * (q + 1), v[(q + 1) & 1][0]);
-              tmem_ld<J>(taddr + 8 * J * (q + 1) + (16u << 16), v[(q + 1) & 1][1]);
-            } else {  // the last columns are in registers: the accumulator goes back to the MMAs
+            uint32_t v[2][4 * J];  // [16-row half]
+            if (rows_here) {
+              const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + at.slot * NT + part * C::kCols + 8 * J * q;
+              tmem_ld<J>(taddr, v[0]);
+              tmem_ld<J>(taddr + (16u << 16), v[1]);
+              tmem_wait();
+            }
+            if (q == NQ - 1) {  // the last columns are in registers: the accumulator goes back to the MMAs
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&acc_empty[buf]);
+              if (lane == 0) mbar_arrive(&acc_empty[at.slot]);
+              at.next();
             }
+            if (!rows_here) continue;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
               uint64_t cs = 0;
               if constexpr (!BLOCK) cs = *reinterpret_cast<const uint64_t*>(csc + 8 * (J * q + j));
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t* p = &v[q & 1][i >> 1][4 * j + 2 * (i & 1)];
+                const uint32_t* p = &v[i >> 1][4 * j + 2 * (i & 1)];
                 const uint64_t pp = pack2(p[0], p[1]);
                 acc[i][J * q + j] = fma2(BLOCK ? pp : mul2(pp, cs), rs[i], acc[i][J * q + j]);
               }
@@ -415,7 +440,7 @@ constexpr int P_STAGES = 5;
 constexpr int P_STAGE_BYTES = (BM + PN / 2) * BK;  // per CTA
 constexpr int P_EPI_WARPS = 8;
 constexpr int P_THREADS = 128 + P_EPI_WARPS * 32;
-constexpr int P_SG = 4;                            // blocks whose scales are staged at a time
+constexpr int P_SG = SG;
 constexpr int P_SCALE_ROW = 2 * BM;                // floats per block and half: tokens, then its weight rows
 constexpr int P_SCALE_BYTES = 2 * 2 * P_SG * P_SCALE_ROW * 4;  // [half][buffer][block]
 constexpr int P_OUT_BYTES = P_EPI_WARPS * 4096;    // a 32-row x 128-byte tile per warp on its way to Y
@@ -423,6 +448,7 @@ constexpr int P_SMEM = P_STAGES * P_STAGE_BYTES + P_OUT_BYTES + P_SCALE_BYTES + 
 // register split (per thread): warps 0-3 give theirs up to the epilogue, whose sums take 128
 constexpr int kLaunchRegs = 168, kEpiRegs = 232, kOtherRegs = 40;
 static_assert(128 * kOtherRegs + P_EPI_WARPS * 32 * kEpiRegs <= P_THREADS * kLaunchRegs, "register split");
+static_assert(SG == 4, "scales are fetched four blocks at a time");
 static_assert(P_SMEM <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ void umma_f8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -460,7 +486,7 @@ __device__ __forceinline__ void pair_exit_barrier() {
   cluster_sync();
 }
 
-template <bool BLOCK, typename TY>
+template <bool BLOCK, int VEC, typename TY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
                            const __grid_constant__ CUtensorMap map_y, const Args a) {
@@ -476,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();  // 0 leads the pair
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
@@ -503,69 +529,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer (this CTA's halves)
-      if (lane == 0) {
-        uint32_t stage = 0;
-        bool ok = true;
-        const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's stage barriers
-        for (int u = pair; u < a.units && ok; u += n_pairs) {
-          int tt, tw, s;
-          unit_coords(u, a, tt, tw, s);
-          for (int b = 0; b < a.kb; ++b, ++stage) {
-            const uint32_t slot = stage % P_STAGES, round = stage / P_STAGES;
-            if (!mbar_wait(&empty[slot], (round & 1) ^ 1, abort_flag, a.status, 61)) {
-              ok = false;
-              break;
-            }
-            uint8_t* T = smem + slot * P_STAGE_BYTES;
-            const uint32_t bar = full0 + slot * 8;
-            if (rank == 0) mbar_expect_tx(&full[slot], 2 * P_STAGE_BYTES);
+      Ring<P_STAGES> r;
+      uint32_t issued = 0;
+      bool ok = true;
+      const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's stage barriers
+      for (int u = pair; u < a.units && ok; u += n_pairs) {
+        int tt, tw, s;
+        unit_coords(u, a, tt, tw, s);
+        for (int b = 0; b < a.kb; ++b, ++issued, r.next()) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[r.slot], r.parity ^ 1, abort_flag, a.status, 61));
+          if (!ok) break;
+          if (elect_one()) {
+            uint8_t* T = smem + r.slot * P_STAGE_BYTES;
+            const uint32_t bar = full0 + r.slot * 8;
+            if (rank == 0) mbar_expect_tx(&full[r.slot], 2 * P_STAGE_BYTES);
             tma_load_2d_pair(T, &map_t, b * BK, tt * 2 * BM + BM * (int)rank, bar);
             // of each half's 128 weight rows, this CTA's 64
             tma_load_2d_pair(T + BM * BK, &map_w, b * BK, tw * PN + 64 * (int)rank, bar);
             tma_load_2d_pair(T + BM * BK + 64 * BK, &map_w, b * BK, tw * PN + 128 + 64 * (int)rank, bar);
           }
-        }
-        // the copies already issued land before the CTA leaves: the even CTA watches both CTAs' on its stage
-        // barriers, and the cluster barrier at the end keeps the odd CTA resident until then
-        if (!ok && rank == 0) {
-          const uint32_t first = stage > P_STAGES ? stage - P_STAGES : 0;
-          for (uint32_t i = first; i < stage; ++i) mbar_wait_drain_cluster(&full[i % P_STAGES], (i / P_STAGES) & 1);
+          __syncwarp();
         }
       }
+      // the copies already issued land before the CTA leaves: the even CTA watches both CTAs' on its stage
+      // barriers, and the cluster barrier at the end keeps the odd CTA resident until then
+      if (!ok && rank == 0) {
+        const uint32_t first = issued > P_STAGES ? issued - P_STAGES : 0;
+        for (uint32_t i = first; i < issued; ++i) mbar_wait_drain_cluster(&full[i % P_STAGES], (i / P_STAGES) & 1);
+      }
     } else if (warp == 1 || warp == 2) {
-      if (lane == 0 && rank == 0) {
+      if (rank == 0) {
         // -------------------------------------------------------------- MMA issuers (even CTA), one per half
-        const int h = warp - 1;
-        uint32_t stage = 0;
+        const uint32_t h = warp - 1;
+        Ring<P_STAGES> r;
+        Ring<2> acc;
         bool ok = true;
         const uint64_t desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t w_off = (uint64_t)((BM * BK + h * 64 * BK) >> 4);
         for (int u = pair; u < a.units && ok; u += n_pairs) {
-          for (int b = 0; b < a.kb; ++b, ++stage) {
-            const uint32_t slot = stage % P_STAGES, round = stage / P_STAGES, buf = stage & 1, use = stage >> 1;
-            if (!mbar_wait(&acc_empty[2 * buf + h], (use & 1) ^ 1, abort_flag, a.status, 62) ||
-                !mbar_wait(&full[slot], round & 1, abort_flag, a.status, 63)) {
-              ok = false;
-              break;
-            }
+          for (int b = 0; b < a.kb; ++b, r.next(), acc.next()) {
+            const uint32_t half = 2 * acc.slot + h;
+            ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[half], acc.parity ^ 1, abort_flag, a.status, 62) &&
+                                             mbar_wait(&full[r.slot], r.parity, abort_flag, a.status, 63));
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t td = desc0 + (uint64_t)((slot * P_STAGE_BYTES) >> 4);
-  #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)
-              umma_f8_pair(tmem_base + (2 * buf + h) * 128, td + (uint64_t)(kk * 2), td + w_off + (uint64_t)(kk * 2),
-                           a.idesc, kk > 0 ? 1u : 0u);
-            umma_commit_pair(&acc_full[2 * buf + h]);
-            umma_commit_pair(&empty[slot]);
+            if (elect_one()) {
+              const uint64_t td = desc0 + (uint64_t)((r.slot * P_STAGE_BYTES) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < BK / 32; ++kk)
+                umma_f8_pair(tmem_base + half * 128, td + (uint64_t)(kk * 2), td + w_off + (uint64_t)(kk * 2), a.idesc,
+                             kk > 0 ? 1u : 0u);
+              umma_commit_pair(&acc_full[half]);
+              umma_commit_pair(&empty[r.slot]);
+            }
+            __syncwarp();
           }
         }
         // every MMA of the pair is complete before either CTA frees TMEM or leaves
-        umma_commit_pair(drain);
-        mbar_wait_drain(drain, 0);
-      } else if (lane == 0) {
-        mbar_wait_drain(drain, 0);  // odd CTA: the pair's last MMAs are complete
+        if (elect_one()) umma_commit_pair(drain);
+        __syncwarp();
       }
-      __syncwarp();
+      mbar_wait_drain(drain, 0);  // (the odd CTA waits for the pair's last MMAs too)
     }
+    __syncwarp();
     tc_fence_before();
     pair_exit_barrier();
     if (warp == 1) {
@@ -581,7 +607,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     const int r4 = lane >> 2, c4 = 2 * (lane & 3);
     const uint32_t acc_empty0 = mapa_shared(acc_empty, 0);
     uint8_t* out_tile = out_tiles + (warp - 4) * 4096;
-    uint32_t stage = 0, group = 0;
+    uint32_t group = 0;
+    Ring<2> at;  // the accumulator of the block in hand
     bool ok = true;  // as in the single-CTA kernel: no warp leaves the walk, the named barrier needs all
     for (int u = pair; u < a.units; u += n_pairs) {
       int tt, tw, s;
@@ -593,13 +620,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
                                : a.b_scales + (int64_t)min(w0 + et, a.n - 1) * a.kb;
       float t_next[P_SG], w_next[P_SG];
       auto fetch = [&](int g0) {
-        fetch_scales<P_SG>(tsc, g0, a.kb, a.vec_scales, t_next);
-        fetch_scales<P_SG>(wsc, g0, a.kb, a.vec_scales, w_next);
+        fetch_scales<VEC>(tsc, g0, a.kb, t_next);
+        fetch_scales<VEC>(wsc, g0, a.kb, w_next);
       };
       fetch(0);
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      uint32_t v[2][16];
+      auto load = [&](int q) {
+        const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + (2 * at.slot + half) * 128 + 16 * q;
+        if constexpr (BLOCK) {
+          tmem_ld_rows(taddr, v[q & 1]);
+        } else {
+          tmem_ld<2>(taddr, v[q & 1]);
+          tmem_ld<2>(taddr + (16u << 16), v[q & 1] + 8);
+        }
+      };
+      auto begin_block = [&]() {
+        if (ok) ok = mbar_wait(&acc_full[2 * at.slot + half], at.parity, abort_flag, a.status, 66);
+        tc_fence_after();
+        load(0);
+      };
+      begin_block();
       for (int g0 = 0; g0 < a.kb; g0 += P_SG, ++group) {
         float* sc = staged + (half * 2 + (group & 1)) * P_SG * P_SCALE_ROW;  // the other buffer may still be read
 #pragma unroll
@@ -610,60 +653,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         fetch(g0 + P_SG);
         asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
         const int g1 = min(a.kb, g0 + P_SG);
-        for (int b = g0; b < g1; ++b, ++stage, sc += P_SCALE_ROW) {
-          const uint32_t buf = stage & 1, use = stage >> 1;
-          const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + (2 * buf + half) * 128;
-          if constexpr (BLOCK) {
-            const uint32_t rs1 = __float_as_uint(sc[32 * quad + lane]);
-            const uint64_t rs = pack2(rs1, rs1);
-            if (ok) ok = mbar_wait(&acc_full[2 * buf + half], use & 1, abort_flag, a.status, 66);
-            tc_fence_after();
-            uint32_t v[2][16];
-            tmem_ld_rows(taddr, v[0]);
+        for (int b = g0; b < g1; ++b, sc += P_SCALE_ROW) {
+          uint64_t rs[BLOCK ? 1 : 4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              tmem_wait();
-              if (q < 7) {  // the next columns are on their way from TMEM while these are added
-                tmem_ld_rows(taddr + 16 * (q + 1), v[(q + 1) & 1]);
-              } else {      // the last columns are in registers: the accumulator goes back to the MMAs
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(acc_empty0 + (2 * buf + half) * 8);
-              }
+          for (int i = 0; i < (BLOCK ? 1 : 4); ++i) {
+            const uint32_t r = __float_as_uint(sc[BLOCK ? 32 * quad + lane : 32 * quad + r4 + 8 * i]);
+            rs[i] = pack2(r, r);
+          }
+          const float* csc = sc + BM + c4;
+          // loads from TMEM run one step ahead, across blocks
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            tmem_wait();
+            if (q < 7) {
+              load(q + 1);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_relaxed(acc_empty0 + (2 * at.slot + half) * 8);
+              at.next();
+              if (b + 1 < a.kb) begin_block();
+            }
+            if constexpr (BLOCK) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                acc[8 * q + i] = fma2(pack2(v[q & 1][2 * i], v[q & 1][2 * i + 1]), rs, acc[8 * q + i]);
-            }
-          } else {
-            uint64_t rs[4];
+                acc[8 * q + i] = fma2(pack2(v[q & 1][2 * i], v[q & 1][2 * i + 1]), rs[0], acc[8 * q + i]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t v = __float_as_uint(sc[32 * quad + r4 + 8 * i]);
-              rs[i] = pack2(v, v);
-            }
-            const float* csc = sc + BM + c4;
-            if (ok) ok = mbar_wait(&acc_full[2 * buf + half], use & 1, abort_flag, a.status, 66);
-            tc_fence_after();
-            uint32_t v[2][8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              tmem_ld<2>(taddr + 16 * q, v[0]);
-              tmem_ld<2>(taddr + 16 * q + (16u << 16), v[1]);
-              const uint64_t cs[2] = {*reinterpret_cast<const uint64_t*>(csc + 16 * q),
-                                      *reinterpret_cast<const uint64_t*>(csc + 16 * q + 8)};
-              tmem_wait();
-              if (q == 7) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(acc_empty0 + (2 * buf + half) * 8);
-              }
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
+              for (int j = 0; j < 2; ++j) {
+                const uint64_t cs = *reinterpret_cast<const uint64_t*>(csc + 8 * (2 * q + j));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const uint32_t* p = &v[i >> 1][4 * j + 2 * (i & 1)];
-                  acc[16 * i + 2 * q + j] = fma2(mul2(pack2(p[0], p[1]), cs[j]), rs[i], acc[16 * i + 2 * q + j]);
+                  const uint32_t* p = &v[q & 1][8 * (i >> 1) + 4 * j + 2 * (i & 1)];
+                  acc[16 * i + 2 * q + j] = fma2(mul2(pack2(p[0], p[1]), cs), rs[BLOCK ? 0 : i], acc[16 * i + 2 * q + j]);
                 }
+              }
             }
           }
         }
@@ -735,6 +759,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     tc_fence_before();
     pair_exit_barrier();
   }
+}
+
+// ------------------------------------------------------------------------------------------------
+// A few tokens (up to 8).  The weights' bytes are all that counts, and a tile's way through tensor maps, TMEM and a
+// second launch for split sums takes longer than reading them (1 x 4096 x 4096: 9.9 us).  Here a CTA takes 16
+// weight rows, its 8 warps the blocks in turn; codes go straight from global memory into registers, two
+// blocks ahead, become fp16 pairs (exact) and fragments of mma.m16n8k16 with the weights on the M
+// side; the warps' scaled sums meet in shared memory, added in order.
+constexpr int kFewTokens = 8;
+constexpr int kFewWarps = 8;
+constexpr int kFewBlocks = 2;  // blocks a warp works on while as many are on their way
+
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A lane holds columns 16 t .. 16 t + 15 of each half of a block, of weight rows g and g + 8 and of token g; which
+// columns meet in one MMA is free as long as both operands agree.
+template <bool BLOCK, typename TY>
+__global__ void __launch_bounds__(kFewWarps * 32, 2) fp8_matmul_few_kernel(const uint8_t* __restrict__ A,
+                                                                           const float* __restrict__ a_scales,
+                                                                           const uint8_t* __restrict__ B,
+                                                                           const float* __restrict__ b_scales, int m,
+                                                                           int n, int k, int kb, TY* __restrict__ Y) {
+  __shared__ float sums[kFewWarps][16][kFewTokens + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int row0 = blockIdx.x * 16;
+  const int r0 = min(row0 + g, n - 1), r1 = min(row0 + g + 8, n - 1);
+  const uint8_t* w0 = B + (int64_t)r0 * k + 16 * t;
+  const uint8_t* w1 = B + (int64_t)r1 * k + 16 * t;
+  const float* s0 = b_scales + (int64_t)(BLOCK ? r0 >> 7 : r0) * kb;
+  const float* s1 = b_scales + (int64_t)(BLOCK ? r1 >> 7 : r1) * kb;
+  const uint8_t* x = A + (int64_t)g * k + 16 * t;
+  const bool token_here = g < m;
+  const float* e0 = a_scales + (int64_t)min(2 * t, m - 1) * kb;
+  const float* e1 = a_scales + (int64_t)min(2 * t + 1, m - 1) * kb;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 next[kFewBlocks][4];
+  auto load = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < kFewBlocks; ++i) {
+      const int c = (b0 + i * kFewWarps) * BK;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = c + 64 * h + 16 * t < k;
+        next[i][2 * h] = ok ? __ldg(reinterpret_cast<const uint4*>(w0 + c + 64 * h)) : zero;
+        next[i][2 * h + 1] = ok ? __ldg(reinterpret_cast<const uint4*>(w1 + c + 64 * h)) : zero;
+      }
+    }
+  };
+  load(warp);
+  for (int b0 = warp; b0 < kb; b0 += kFewWarps * kFewBlocks) {
+    uint4 w[kFewBlocks][4];
+#pragma unroll
+    for (int i = 0; i < kFewBlocks; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i][j] = next[i][j];
+    load(b0 + kFewWarps * kFewBlocks);
+#pragma unroll
+    for (int i = 0; i < kFewBlocks; ++i) {
+      const int b = b0 + i * kFewWarps;
+      if (b >= kb) break;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = token_here && b * BK + 64 * h + 16 * t < k;
+        const uint4 xv = ok ? __ldg(reinterpret_cast<const uint4*>(x + b * BK + 64 * h)) : zero;
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+        const uint4 u0 = w[i][2 * h], u1 = w[i][2 * h + 1];
+        const uint32_t a0[4] = {u0.x, u0.y, u0.z, u0.w}, a1[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p0, p1, p2, p3, y0, y1;
+          e4m3_to_f16(a0[q], p0, p2);
+          e4m3_to_f16(a1[q], p1, p3);
+          e4m3_to_f16(xw[q], y0, y1);
+          mma_f16(sum, p0, p1, p2, p3, y0, y1);
+        }
+      }
+      const float f0 = __ldg(s0 + b), f1 = __ldg(s1 + b), c0 = __ldg(e0 + b), c1 = __ldg(e1 + b);
+      acc[0] = fmaf(sum[0] * c0, f0, acc[0]);
+      acc[1] = fmaf(sum[1] * c1, f0, acc[1]);
+      acc[2] = fmaf(sum[2] * c0, f1, acc[2]);
+      acc[3] = fmaf(sum[3] * c1, f1, acc[3]);
+    }
+  }
+  sums[warp][g][2 * t] = acc[0], sums[warp][g][2 * t + 1] = acc[1];
+  sums[warp][g + 8][2 * t] = acc[2], sums[warp][g + 8][2 * t + 1] = acc[3];
+  __syncthreads();
+  if (threadIdx.x < 16 * m) {  // at most 128
+    const int r = threadIdx.x & 15, tok = threadIdx.x >> 4;
+    if (row0 + r < n) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) s += sums[w][r][tok];
+      Y[(int64_t)tok * n + row0 + r] = from_f32<TY>(s);
+    }
+  }
+}
+
+template <typename TY>
+gptq_status launch_few(const void* A, const float* a_scales, const void* B, const float* b_scales, bool block, int m,
+                       int n, int k, TY* Y, cudaStream_t s) {
+  const uint8_t *a = static_cast<const uint8_t*>(A), *b = static_cast<const uint8_t*>(B);
+  const unsigned grid = (unsigned)((n + 15) / 16);
+  const int kb = (k + BK - 1) / BK;
+  if (block)
+    fp8_matmul_few_kernel<true, TY><<<grid, kFewWarps * 32, 0, s>>>(a, a_scales, b, b_scales, m, n, k, kb, Y);
+  else
+    fp8_matmul_few_kernel<false, TY><<<grid, kFewWarps * 32, 0, s>>>(a, a_scales, b, b_scales, m, n, k, kb, Y);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
 }
 
 // Y = the splits' partial sums, added in split order.
@@ -817,7 +964,9 @@ bool out_map(CUtensorMap* map, void* base, int64_t m, int64_t n) {
 
 template <int NT, bool BLOCK, typename TY>
 gptq_status launch(const CUtensorMap& t, const CUtensorMap& w, Args a, int sms, cudaStream_t s) {
-  auto kernel = fp8_matmul_kernel<NT, BLOCK, TY>;
+  auto kernel = a.scale_width == 4   ? fp8_matmul_kernel<NT, BLOCK, 4, TY>
+                : a.scale_width == 2 ? fp8_matmul_kernel<NT, BLOCK, 2, TY>
+                                     : fp8_matmul_kernel<NT, BLOCK, 1, TY>;
   // D fp32 (bit 4), A and B e4m3 (0), both K-major, N = NT, M = 128
   a.idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
   GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmem));
@@ -830,7 +979,9 @@ template <bool BLOCK, typename TY>
 gptq_status launch_pair(const CUtensorMap& t, const CUtensorMap& w, Args a, int sms, cudaStream_t s) {
   CUtensorMap y = t;  // not used unless Y's rows are aligned
   if (a.vec_y && !out_map<TY>(&y, a.Y, a.m, a.n)) return GPTQ_ERR_CUDA;
-  auto kernel = fp8_matmul_pair_kernel<BLOCK, TY>;
+  auto kernel = a.scale_width == 4   ? fp8_matmul_pair_kernel<BLOCK, 4, TY>
+                : a.scale_width == 2 ? fp8_matmul_pair_kernel<BLOCK, 2, TY>
+                                     : fp8_matmul_pair_kernel<BLOCK, 1, TY>;
   a.idesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)((2 * BM) >> 4) << 24);
   cudaFuncAttributes attr;  // the register split draws on the launch's registers: never ask for more than those
   GPTQ_CUDA_TRY(cudaFuncGetAttributes(&attr, kernel));
@@ -867,7 +1018,9 @@ gptq_status launch_typed(const Plan& p, bool block, const CUtensorMap& t, const 
 
 }  // namespace
 
+
 size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k) {
+  if (m <= kFewTokens) return 0;
   const Plan p = make_plan(m, n, k);
   return p.splits > 1 ? align_up((size_t)p.splits * m * n * sizeof(float), 256) : 0;
 }
@@ -875,6 +1028,14 @@ size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k) {
 gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* B, const float* b_scales,
                               int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* Y, int32_t y_dtype,
                               int32_t* status, void* workspace, cudaStream_t stream) {
+  if (m <= kFewTokens) {
+    const bool block = b_block_rows == 128;
+    switch (y_dtype) {
+      case GPTQ_BF16: return launch_few(A, a_scales, B, b_scales, block, (int)m, (int)n, (int)k, static_cast<__nv_bfloat16*>(Y), stream);
+      case GPTQ_FP16: return launch_few(A, a_scales, B, b_scales, block, (int)m, (int)n, (int)k, static_cast<__half*>(Y), stream);
+      default: return launch_few(A, a_scales, B, b_scales, block, (int)m, (int)n, (int)k, static_cast<float*>(Y), stream);
+    }
+  }
   const Plan p = make_plan(m, n, k);
   const int64_t units = (int64_t)p.tiles_w * p.tiles_t * p.splits;
   if (units > 0x7fffffff - kPlanSMs) return GPTQ_ERR_ARG;
@@ -889,7 +1050,10 @@ gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* 
   a.tiles_w = p.tiles_w, a.tiles_t = p.tiles_t, a.units = (int)units;
   a.kb_per_split = p.kb_per_split;
   a.token_bytes = token_rows * BK;
-  a.vec_scales = p.kb % 4 == 0 && aligned(a_scales, 16) && aligned(b_scales, 16);
+  a.scale_width = 4;
+  while (a.scale_width > 1 && (p.kb % a.scale_width || !aligned(a_scales, 4 * a.scale_width) ||
+                               !aligned(b_scales, 4 * a.scale_width)))
+    a.scale_width /= 2;
   a.vec_y = n * (y_dtype == GPTQ_FP32 ? 4 : 2) % 16 == 0 && aligned(Y, 16);
   const bool block = b_block_rows == 128;
   a.a_scales = a_scales, a.b_scales = b_scales;
