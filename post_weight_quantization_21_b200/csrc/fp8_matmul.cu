@@ -694,6 +694,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       }
       if (!ok) continue;
       const int row0 = t0 + 32 * quad;
+      int rr = r4, cc = c4;  // opaque: addresses computed here, not kept in registers through the blocks
+      asm volatile("" : "+r"(rr), "+r"(cc));
       if (a.vec_y) {
         // through shared memory as 32 rows x 128 bytes (16-byte chunks swizzled by the row, as the copy
         // expects), then asynchronously to Y; what lies past Y's edges is not written.  Stores straight
@@ -723,8 +725,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
               for (int j = 0; j < OC / 8; ++j) {
                 float v0, v1;
                 unpack2(acc[16 * i + o * (OC / 8) + j], v0, v1);
-                const int byte = (8 * j + c4) * (int)sizeof(TY);
-                TY* y = reinterpret_cast<TY*>(out_tile + (r4 + 8 * i) * 128 + ((byte >> 4 ^ r4) << 4) + (byte & 15));
+                const int byte = (8 * j + cc) * (int)sizeof(TY);
+                TY* y = reinterpret_cast<TY*>(out_tile + (rr + 8 * i) * 128 + ((byte >> 4 ^ rr) << 4) + (byte & 15));
                 store_pair(y, v0, v1, 2, true);
               }
           }
@@ -742,7 +744,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         const bool even = (a.n & 1) == 0;  // rows start on pairs
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int tok = row0 + r4 + 8 * i, w = w0 + c4;
+          const int tok = row0 + rr + 8 * i, w = w0 + cc;
           if (tok >= a.m) continue;
           TY* y = static_cast<TY*>(a.Y) + (int64_t)tok * a.n + w;
 #pragma unroll
