@@ -61,7 +61,8 @@ struct Args {
   const float* a_scales;
   const float* b_scales;
   void* Y;
-  float* partial;                  // [split][m][n] when the blocks are split, else null
+  float* partial;                  // [split][m][ld] when the blocks are split, else null
+  int ld, splits;
   int32_t* status;
 };
 
@@ -396,13 +397,13 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
         }
       }
       if (ok && rows_here) {
-        const bool even = (a.n & 1) == 0;  // rows start on pairs
+        const bool even = a.partial || (a.n & 1) == 0;  // rows start on pairs
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tok = t0 + 32 * quad + r4 + 8 * i;
           if (tok >= a.m) continue;
           const int w = w0 + part * C::kCols + c4;
-          const int64_t at = ((int64_t)s * (a.partial ? a.m : 0) + tok) * a.n + w;
+          const int64_t at = a.partial ? ((int64_t)s * a.m + tok) * a.ld + w : (int64_t)tok * a.n + w;
 #pragma unroll
           for (int j = 0; j < C::kCols / 8; ++j) {
             float v0, v1;
@@ -486,6 +487,14 @@ __device__ __forceinline__ void pair_exit_barrier() {
   cluster_sync();
 }
 
+// shared -> global copy of a tile of a stack of matrices
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+
 template <bool BLOCK, int VEC, typename TY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w,
@@ -536,7 +545,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       for (int u = pair; u < a.units && ok; u += n_pairs) {
         int tt, tw, s;
         unit_coords(u, a, tt, tw, s);
-        for (int b = 0; b < a.kb; ++b, ++issued, r.next()) {
+        const int b1 = min(a.kb, (s + 1) * a.kb_per_split);
+        for (int b = s * a.kb_per_split; b < b1; ++b, ++issued, r.next()) {
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[r.slot], r.parity ^ 1, abort_flag, a.status, 61));
           if (!ok) break;
           if (elect_one()) {
@@ -567,7 +577,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         const uint64_t desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t w_off = (uint64_t)((BM * BK + h * 64 * BK) >> 4);
         for (int u = pair; u < a.units && ok; u += n_pairs) {
-          for (int b = 0; b < a.kb; ++b, r.next(), acc.next()) {
+          int tt, tw, s;
+          unit_coords(u, a, tt, tw, s);
+          const int nb = min(a.kb, (s + 1) * a.kb_per_split) - s * a.kb_per_split;
+          for (int b = 0; b < nb; ++b, r.next(), acc.next()) {
             const uint32_t half = 2 * acc.slot + h;
             ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[half], acc.parity ^ 1, abort_flag, a.status, 62) &&
                                              mbar_wait(&full[r.slot], r.parity, abort_flag, a.status, 63));
@@ -613,6 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     for (int u = pair; u < a.units; u += n_pairs) {
       int tt, tw, s;
       unit_coords(u, a, tt, tw, s);
+      const int b0 = s * a.kb_per_split, b1 = min(a.kb, b0 + a.kb_per_split);
       const int t0 = tt * 2 * BM + BM * (int)rank, w0 = tw * PN + 128 * half;
       // scales staged P_SG blocks at a time, each half its own; BLOCK: the tokens' times the weight rows' one
       const float* tsc = a.a_scales + (int64_t)min(t0 + et, a.m - 1) * a.kb;
@@ -623,7 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         fetch_scales<VEC>(tsc, g0, a.kb, t_next);
         fetch_scales<VEC>(wsc, g0, a.kb, w_next);
       };
-      fetch(0);
+      fetch(b0);
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
@@ -643,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         load(0);
       };
       begin_block();
-      for (int g0 = 0; g0 < a.kb; g0 += P_SG, ++group) {
+      for (int g0 = b0; g0 < b1; g0 += P_SG, ++group) {
         float* sc = staged + (half * 2 + (group & 1)) * P_SG * P_SCALE_ROW;  // the other buffer may still be read
 #pragma unroll
         for (int i = 0; i < P_SG; ++i) {
@@ -652,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         }
         fetch(g0 + P_SG);
         asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-        const int g1 = min(a.kb, g0 + P_SG);
+        const int g1 = min(b1, g0 + P_SG);
         for (int b = g0; b < g1; ++b, sc += P_SCALE_ROW) {
           uint64_t rs[BLOCK ? 1 : 4];
 #pragma unroll
@@ -672,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive_relaxed(acc_empty0 + (2 * at.slot + half) * 8);
               at.next();
-              if (b + 1 < a.kb) begin_block();
+              if (b + 1 < b1) begin_block();
             }
             if constexpr (BLOCK) {
 #pragma unroll
@@ -733,7 +747,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && row0 < a.m && w0 + o * OC < a.n) {
-            tma_store_2d(&map_y, w0 + o * OC, row0, out_tile);
+            tma_store_3d(&map_y, w0 + o * OC, row0, s, out_tile);
             bulk_commit();
           }
         }
@@ -886,14 +900,17 @@ gptq_status launch_few(const void* A, const float* a_scales, const void* B, cons
   return GPTQ_OK;
 }
 
-// Y = the splits' partial sums, added in split order.
+// Y = the splits' partial sums, added in split order; their rows are ld floats apart.
 template <typename TY>
-__global__ void __launch_bounds__(256) fp8_matmul_reduce_kernel(const float* __restrict__ partial, int splits,
-                                                                int64_t n, TY* __restrict__ Y) {
-  for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
+__global__ void __launch_bounds__(256) fp8_matmul_reduce_kernel(const float* __restrict__ partial, int splits, int m,
+                                                                int n, int ld, TY* __restrict__ Y) {
+  const int64_t plane = (int64_t)m * ld;
+  for (int r = blockIdx.y; r < m; r += gridDim.y) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= n) continue;
     float s = 0.0f;
-    for (int t = 0; t < splits; ++t) s += partial[t * n + e];
-    Y[e] = from_f32<TY>(s);
+    for (int t = 0; t < splits; ++t) s += partial[t * plane + (int64_t)r * ld + c];
+    Y[(int64_t)r * n + c] = from_f32<TY>(s);
   }
 }
 
@@ -901,38 +918,38 @@ struct Plan {
   int nt, tiles_t, tiles_w, kb, kb_per_split, splits;  // nt = 256: the pair form
 };
 
-// Form, tile width and split of the blocks with the lowest estimated time in cycles: a block costs an SM
-// 256 + 2 NT (its operands' way into and out of shared memory), a unit 1500 for its fill and its epilogue,
-// and split sums are written and read back at about 3000 bytes per cycle of the whole GPU plus a launch.
-Plan make_plan(int64_t m, int64_t n, int64_t k) {
+// Form, tile width and split of the blocks with the lowest estimated time in cycles, from times of single sizes: a
+// block takes a CTA of the single form 480 + 3.6 NT (the epilogue's way through TMEM; NT = 32, 64, 128:
+// 17 x 4096 x 4096 in 12.8, 15.7, 17.3 us) and a pair 1100 for four times the widest tile's area (1600 with a scale per weight row); a unit takes 2000 or
+// 6000 for its fill and its end; split sums are written and read back at about 3000 bytes per cycle of the
+// whole GPU, plus a launch.
+Plan make_plan(int64_t m, int64_t n, int64_t k, bool block) {
   Plan best = {};
   double best_cost = 1e300;
   const int kb = (int)((k + BK - 1) / BK);
-  // splits start on multiples of 4 blocks so that their scales' 16-byte loads stay aligned
-  for (int nt = 32; nt <= 128; nt *= 2) {
-    const int64_t tw = (n + nt - 1) / nt, tt = (m + BM - 1) / BM;
+  auto consider = [&](int nt, int64_t tt, int64_t tw, int ctas, double block, double unit) {
     for (int want = 1; want <= 16 && want <= kb; ++want) {
+      // splits start on multiples of 4 blocks so that their scales' 16-byte loads stay aligned
       const int per = want == 1 ? kb : ((kb + want - 1) / want + 3) / 4 * 4, splits = (kb + per - 1) / per;
       if (splits != want) continue;
-      const int64_t units = tw * tt * splits;
-      if (splits > 1 && units > 2 * kPlanSMs) continue;
-      const double waves = (double)((units + kPlanSMs - 1) / kPlanSMs);
-      double cost = waves * (per * (256.0 + 2.0 * nt) + 1500.0);
-      if (splits > 1) cost += 8.0 * splits * (double)m * (double)n / 3000.0 + 4000.0;
+      const int64_t units = tt * tw * splits;
+      if (splits > 1 && units > 2 * kPlanSMs / ctas) continue;
+      const double waves = (double)((units + kPlanSMs / ctas - 1) / (kPlanSMs / ctas));
+      double cost = waves * (per * block + unit);
+      if (splits > 1) cost += 8.0 * splits * (double)m * (double)n / 3000.0 + 5700.0;
       if (cost < best_cost) {
         best_cost = cost;
         best = {nt, (int)tt, (int)tw, kb, per, splits};
       }
     }
-  }
-  if (m > BM) {
-    const int64_t tw = (n + PN - 1) / PN, tt = (m + 2 * BM - 1) / (2 * BM);
-    const double waves = (double)((tw * tt + kPlanSMs / 2 - 1) / (kPlanSMs / 2));
-    const double cost = waves * (kb * 800.0 + 4000.0);
-    if (cost < best_cost) best = {PN, (int)tt, (int)tw, kb, kb, 1};
-  }
+  };
+  for (int nt = 32; nt <= 128; nt *= 2) consider(nt, (m + BM - 1) / BM, (n + nt - 1) / nt, 1, 480.0 + 3.6 * nt, 2000.0);
+  if (m > BM) consider(PN, (m + 2 * BM - 1) / (2 * BM), (n + PN - 1) / PN, 2, block ? 1100.0 : 1600.0, 6000.0);
   return best;
 }
+
+// the split sums' row stride: rows on 16 bytes, as the pair form's copies need them
+int64_t partial_stride(int64_t n) { return (n + 3) / 4 * 4; }
 
 // [rows, k] bytes in boxes of box_rows x 128 with the 128-byte swizzle; rows and columns past the edges read 0
 bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, int box_rows) {
@@ -947,19 +964,19 @@ bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Y in tiles of 32 rows x 128 bytes with the 128-byte swizzle
+// Y, or the split sums as a stack of matrices, in tiles of 32 rows x 128 bytes with the 128-byte swizzle
 template <typename TY>
-bool out_map(CUtensorMap* map, void* base, int64_t m, int64_t n) {
+bool out_map(CUtensorMap* map, void* base, int64_t m, int64_t n, int64_t ld, int64_t stack) {
   auto encode = encode_fn();
   if (encode == nullptr) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)m};
-  const cuuint64_t strides[1] = {(cuuint64_t)(n * sizeof(TY))};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(TY)), 32};
-  const cuuint32_t elem[2] = {1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)n, (cuuint64_t)m, (cuuint64_t)stack};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * sizeof(TY)), (cuuint64_t)(m * ld * sizeof(TY))};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(TY)), 32, 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
   const CUtensorMapDataType type = std::is_same<TY, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : std::is_same<TY, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return encode(map, type, 2, base, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return encode(map, type, 3, base, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -980,7 +997,7 @@ gptq_status launch(const CUtensorMap& t, const CUtensorMap& w, Args a, int sms, 
 template <bool BLOCK, typename TY>
 gptq_status launch_pair(const CUtensorMap& t, const CUtensorMap& w, Args a, int sms, cudaStream_t s) {
   CUtensorMap y = t;  // not used unless Y's rows are aligned
-  if (a.vec_y && !out_map<TY>(&y, a.Y, a.m, a.n)) return GPTQ_ERR_CUDA;
+  if (a.vec_y && !out_map<TY>(&y, a.Y, a.m, a.n, a.partial ? a.ld : a.n, a.splits)) return GPTQ_ERR_CUDA;
   auto kernel = a.scale_width == 4   ? fp8_matmul_pair_kernel<BLOCK, 4, TY>
                 : a.scale_width == 2 ? fp8_matmul_pair_kernel<BLOCK, 2, TY>
                                      : fp8_matmul_pair_kernel<BLOCK, 1, TY>;
@@ -1008,12 +1025,19 @@ gptq_status launch_typed(const Plan& p, bool block, const CUtensorMap& t, const 
     case 32: st = launch_block<32, TY>(block, t, w, a, sms, s); break;
     case 64: st = launch_block<64, TY>(block, t, w, a, sms, s); break;
     case 128: st = launch_block<128, TY>(block, t, w, a, sms, s); break;
-    default: st = block ? launch_pair<true, TY>(t, w, a, sms, s) : launch_pair<false, TY>(t, w, a, sms, s); break;
+    default: {
+      if (a.partial == nullptr) {
+        st = block ? launch_pair<true, TY>(t, w, a, sms, s) : launch_pair<false, TY>(t, w, a, sms, s);
+      } else {  // split sums: fp32, in rows that the copies can write
+        Args b = a;
+        b.Y = a.partial, b.vec_y = true;
+        st = block ? launch_pair<true, float>(t, w, b, sms, s) : launch_pair<false, float>(t, w, b, sms, s);
+      }
+    }
   }
   if (st != GPTQ_OK || a.partial == nullptr) return st;
-  const int64_t e = (int64_t)a.m * a.n;
-  const unsigned blocks = (unsigned)std::min<int64_t>((e + 255) / 256, kPlanSMs * 8);
-  fp8_matmul_reduce_kernel<TY><<<blocks, 256, 0, s>>>(a.partial, p.splits, e, static_cast<TY*>(a.Y));
+  const dim3 grid((unsigned)((a.n + 255) / 256), (unsigned)std::min(a.m, 1024));
+  fp8_matmul_reduce_kernel<TY><<<grid, 256, 0, s>>>(a.partial, a.splits, a.m, a.n, a.ld, static_cast<TY*>(a.Y));
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -1023,8 +1047,12 @@ gptq_status launch_typed(const Plan& p, bool block, const CUtensorMap& t, const 
 
 size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k) {
   if (m <= kFewTokens) return 0;
-  const Plan p = make_plan(m, n, k);
-  return p.splits > 1 ? align_up((size_t)p.splits * m * n * sizeof(float), 256) : 0;
+  size_t need = 0;  // for either kind of weight scales
+  for (int block = 0; block < 2; ++block) {
+    const Plan p = make_plan(m, n, k, block != 0);
+    if (p.splits > 1) need = std::max(need, align_up((size_t)p.splits * m * partial_stride(n) * sizeof(float), 256));
+  }
+  return need;
 }
 
 gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* B, const float* b_scales,
@@ -1038,7 +1066,7 @@ gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* 
       default: return launch_few(A, a_scales, B, b_scales, block, (int)m, (int)n, (int)k, static_cast<float*>(Y), stream);
     }
   }
-  const Plan p = make_plan(m, n, k);
+  const Plan p = make_plan(m, n, k, b_block_rows == 128);
   const int64_t units = (int64_t)p.tiles_w * p.tiles_t * p.splits;
   if (units > 0x7fffffff - kPlanSMs) return GPTQ_ERR_ARG;
   const int token_rows = (int)std::min<int64_t>(BM, (m + 7) / 8 * 8);  // whole swizzle atoms of 8 rows
@@ -1061,6 +1089,7 @@ gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* 
   a.a_scales = a_scales, a.b_scales = b_scales;
   a.Y = Y;
   a.partial = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  a.ld = (int)partial_stride(n), a.splits = p.splits;
   a.status = status;
   switch (y_dtype) {
     case GPTQ_BF16: return launch_typed<__nv_bfloat16>(p, block, t, w, a, sms, stream);

@@ -144,7 +144,8 @@ def _check_matmul(Y, A, sa, B, sb, rows):
 
 # token counts around each tile width, weight rows around a tile, block counts with a cut-off last block
 SHAPES = [(1, 1, 16), (1, 128, 128), (2, 129, 144), (16, 64, 4096), (17, 300, 256), (33, 4096, 1040), (65, 127, 2176),
-          (129, 513, 384), (257, 1000, 1536), (1, 12288, 4096), (640, 4097, 512), (2048, 2304, 272)]
+          (129, 513, 384), (257, 1000, 1536), (1, 12288, 4096), (640, 4097, 512), (2048, 2304, 272), (8, 300, 1040), (9, 300, 1040), (333, 1000, 4224), (257, 770, 6528),
+          (300, 4104, 11008), (385, 512, 2192)]
 
 
 @pytest.mark.parametrize("rows", [1, 128])
