@@ -9,7 +9,11 @@ section 01: each layer is solved on its own inputs).  For one block:
      (q, k and v share their input, so they share one Hessian);
   2. solve every linear layer with gptq_prepare_uinv / gptq_quantize_layer / gptq_pack;
   3. run the block again with the dequantized weights (gptq_dequantize): its outputs are the next
-     block's calibration inputs.
+     block's calibration inputs.  With BlockConfig.linears = "fp8" its linear layers run as they would be
+     served to long prompts instead: the codes as e4m3 integers (gptq_fp8_from_packed, exact), the
+     activations rounded to e4m3 with a scale per token and 128 channels (gptq_fp8_quantize), the products
+     on the fp8 tensor cores (gptq_fp8_matmul), so that the next blocks are calibrated on what those
+     products give.
 
 The block is an OPT-style pre-LayerNorm decoder block (the pages' models are OPT, BLOOM and LLaMA; the
 pages do not fix a block, so the plainest one is used): h = x + Wo attn(LN1(x)), y = h + W2 relu(W1
@@ -41,6 +45,13 @@ class BlockConfig:
     group_size: int = 0
     block_size: int = 128
     damp: float = 0.01
+    linears: str = "dense"  # products of the quantized forward: "dense" (dequantized weights) or "fp8"
+
+    def __post_init__(self):
+        if self.linears not in ("dense", "fp8"):
+            raise ValueError(f"linears {self.linears!r}: 'dense' or 'fp8'")
+        if self.linears == "fp8" and self.group_size % 128:
+            raise ValueError(f"fp8 products take one scale per 128 channels: group_size {self.group_size}")
 
     def shape(self, name: str) -> tuple[int, int]:
         """[out_features, in_features] of a linear layer."""
@@ -64,19 +75,21 @@ def make_block(cfg: BlockConfig, seed: int, device="cpu") -> dict[str, torch.Ten
 
 
 def block_forward(cfg: BlockConfig, p: dict[str, torch.Tensor], x: torch.Tensor, collect=None,
-                  weights: dict[str, torch.Tensor] | None = None) -> torch.Tensor:
+                  weights: dict[str, torch.Tensor] | None = None, products=None) -> torch.Tensor:
     """y = block(x) for x [n_seq * seq_len, d] (fp32 math).  ``collect(name, act)`` is called with the
     input of every linear group (INPUTS) as it is produced; ``weights`` overrides the linear weights
-    (the dequantized ones)."""
-    W = {n: (weights[n] if weights is not None else p[n]).float() for n in LINEARS}
+    (the dequantized ones); ``products(names, x)`` overrides the products themselves: one [tokens, out_features]
+    result per name for the layers ``names`` that share the input x."""
+    W = {} if products is not None else {n: (weights[n] if weights is not None else p[n]).float() for n in LINEARS}
     d, H = cfg.d_model, cfg.n_heads
     x = x.float()
     a_in = torch.nn.functional.layer_norm(x, (d,), p["ln1_g"], p["ln1_b"])
     if collect:
         collect("attn_in", a_in)
-    q = a_in @ W["q"].t() + p["q_b"]
-    k = a_in @ W["k"].t() + p["k_b"]
-    v = a_in @ W["v"].t() + p["v_b"]
+    if products is None:
+        def products(names, act):
+            return [act @ W[n].t() for n in names]
+    q, k, v = (y + p[n + "_b"] for n, y in zip("qkv", products(("q", "k", "v"), a_in)))
     S = cfg.seq_len
     n_seq = x.shape[0] // S
 
@@ -87,14 +100,14 @@ def block_forward(cfg: BlockConfig, p: dict[str, torch.Tensor], x: torch.Tensor,
     o_in = att.transpose(1, 2).reshape(n_seq * S, d)
     if collect:
         collect("out_in", o_in)
-    h = x + o_in @ W["out"].t() + p["out_b"]
+    h = x + products(("out",), o_in)[0] + p["out_b"]
     f_in = torch.nn.functional.layer_norm(h, (d,), p["ln2_g"], p["ln2_b"])
     if collect:
         collect("fc1_in", f_in)
-    a = torch.relu(f_in @ W["fc1"].t() + p["fc1_b"])
+    a = torch.relu(products(("fc1",), f_in)[0] + p["fc1_b"])
     if collect:
         collect("fc2_in", a)
-    return h + a @ W["fc2"].t() + p["fc2_b"]
+    return h + products(("fc2",), a)[0] + p["fc2_b"]
 
 
 @dataclasses.dataclass
@@ -104,6 +117,32 @@ class QuantizedLinear:
     zeros: torch.Tensor     # [m, n_groups] int32
     packed: torch.Tensor    # [m, d*b/32] int32
     W_hat: torch.Tensor     # [m, d] fp16, the dequantized weights
+
+
+class Fp8Linears:
+    """Products of a block's quantized layers on the fp8 tensor cores, as block_forward's ``products``."""
+
+    def __init__(self, cfg: BlockConfig, layers: dict[str, QuantizedLinear], status: torch.Tensor):
+        self.status, self.B, self.scales = status, {}, {}
+        for nm, q in layers.items():
+            m, d = cfg.shape(nm)
+            self.B[nm] = torch.empty(m, d, dtype=torch.float8_e4m3fn, device=q.packed.device)
+            self.scales[nm] = torch.empty(m, -(-d // 128), device=q.packed.device)
+            g.gptq_fp8_from_packed(q.packed, q.scales, q.zeros, cfg.bits, cfg.group_size, self.B[nm], self.scales[nm])
+
+    def __call__(self, names, x: torch.Tensor) -> list[torch.Tensor]:
+        n, k = x.shape
+        A = torch.empty(n, k, dtype=torch.float8_e4m3fn, device=x.device)
+        a_scales = torch.empty(n, -(-k // 128), device=x.device)
+        g.gptq_fp8_quantize(x.contiguous(), A, a_scales)
+        out = []
+        for nm in names:
+            m = self.B[nm].shape[0]
+            Y = torch.empty(n, m, device=x.device)
+            ws = torch.empty(max(256, g.gptq_fp8_matmul_workspace_size(n, m, k)), dtype=torch.uint8, device=x.device)
+            g.gptq_fp8_matmul(A, a_scales, self.B[nm], self.scales[nm], 1, Y, self.status, ws)
+            out.append(Y)
+        return out
 
 
 class BlockQuantizer:
@@ -120,8 +159,8 @@ class BlockQuantizer:
         dims = {"attn_in": cfg.d_model, "out_in": cfg.d_model, "fc1_in": cfg.d_model, "fc2_in": cfg.d_ffn}
         self.H = {k: torch.empty(n, n, device=self.dev) for k, n in dims.items()}
         # one status word per call whose failure must survive the later calls: 4 Hessians, 4 prepare
-        # steps, 6 layer solves
-        self.status = torch.zeros(14, 2, dtype=torch.int32, device=self.dev)
+        # steps, 6 layer solves; the last for all fp8 products
+        self.status = torch.zeros(15, 2, dtype=torch.int32, device=self.dev)
         self._row = {**{k: i for i, k in enumerate(INPUTS)}, **{"U_" + k: 4 + i for i, k in enumerate(INPUTS)},
                      **{"Q_" + k: 8 + i for i, k in enumerate(LINEARS)}}
         chunk_tokens = chunk_seqs * cfg.seq_len
@@ -180,9 +219,10 @@ class BlockQuantizer:
         S = cfg.seq_len
         step = self.chunk_seqs * S
         W_hat = {nm: out[nm].W_hat for nm in LINEARS}
+        products = Fp8Linears(cfg, out, self.status[14]) if cfg.linears == "fp8" else None
         Y = torch.empty(X.shape[0], cfg.d_model, dtype=X.dtype, device=self.dev)
         for t0 in range(0, X.shape[0], step):
-            Y[t0:t0 + step] = block_forward(cfg, p, X[t0:t0 + step], weights=W_hat).to(X.dtype)
+            Y[t0:t0 + step] = block_forward(cfg, p, X[t0:t0 + step], weights=W_hat, products=products).to(X.dtype)
         ev[3].record()
         torch.cuda.synchronize(self.dev)
         for word in self.status:
