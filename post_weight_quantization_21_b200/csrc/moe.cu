@@ -9,8 +9,13 @@
 // one AND for two codes, nothing to subtract, and the pair is a ready fragment of mma.m16n8k16 (weights on
 // the M side, up to 8 tokens on the N side: a product with so few columns is no tcgen05 shape, and the tensor
 // pipe has time to spare here).  The order of the columns in a sum is free, so a pair is two codes that lie
-// 16 bits apart (see Pairs) and the tokens' values are laid out to match, multiplied by 2^-p.  The zero point
-// leaves the sum as zero * sum_j x_j, which starts the accumulator: sum_j (q_j - zero) x_j = sum q x - zero sum x.
+// 16 bits apart (see Pairs) and the tokens' values are laid out to match, multiplied by 2^-p.  The
+// zero point leaves the sum as zero * sum_j x_j, which starts the accumulator: sum_j (q_j - zero) x_j = sum q x -
+// zero sum x.  Products are aligned by their operands' exponents before they are added, and a subnormal's
+// exponent says 2^-14 whatever its size, so sums over subnormals keep some seven bits less than they could:
+// results off by 1e-5 to 4e-5, a tenth of fp16's own rounding and less.  For an fp32 Y the codes are therefore
+// joined with the exponent of 1024 and 1024 + zero 2^p is taken off, which leaves (q - zero) 2^p as a normal
+// fp16, exactly: one subtraction more per pair.
 //
 // Tokens become fp16 terms of x 2^-e, e per token and 128 columns so that the largest value lies below 2^15: one
 // term holds a bf16 or fp16 value exactly as long as it is not below 2^-21 of the block's largest (then it is off
@@ -106,6 +111,13 @@ __device__ __forceinline__ void unit_quad<3>(const uint32_t (&w)[3], int q, uint
       v[j] = s % 3 == 0 ? mask_pair<3, 0>(r) : (s % 3 == 1 ? mask_pair<3, 3>(r) : mask_pair<3, 6>(r));
     }
   }
+}
+
+// (q - zero) 2^p of two codes, exact: q 2^p and zero 2^p are the low mantissa bits of 1024 + ...
+__device__ __forceinline__ uint32_t less_zero(uint32_t q, uint32_t zero) {
+  q |= 0x64006400u, zero |= 0x64006400u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&q), *reinterpret_cast<const __half2*>(&zero));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -514,7 +526,8 @@ __device__ __forceinline__ void copies_wait() {
 // columns are scaled into fp32 sums.
 // SUB: scales change inside a chunk (groups of 32 or 64); each quarter then has accumulators of its own and
 // sees the other quarters' tokens as zeros.
-template <int BITS, int TERMS, int NT, int SUB>
+// PRECISE: zero points off the codes (see the top), else through the tokens' sums.
+template <int BITS, int TERMS, int NT, int SUB, bool PRECISE>
 __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_kernel(const ProductArgs a) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float sums[kProductWarps][32][8 * NT + 1];
@@ -721,26 +734,30 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
         const uint8_t* tokens = stage + my_tokens + h * 256;
         const float2* stats = reinterpret_cast<const float2*>(stage + my_tokens + a.cols * (TERMS * 512)) + h;
         const float* unit_sums = reinterpret_cast<const float*>(stage + my_tokens + a.cols * (TERMS * 512 + 16)) + h * 4;
-        // the accumulators start at -zero sum x; row g of an M tile is in values 0 and 1, row g + 8 in 2 and 3
+        // the accumulators start at -zero sum x (PRECISE: at zero); row g of an M tile is in values 0 and 1, row g + 8
+        // in 2 and 3
         float sum[NT][SUB][2][4];
         float2 st[NT][2];
+        uint32_t zp[4];  // PRECISE: this lane's unit's zeros, in both halves
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           if (n == 0 || 8 * n < count) st[n][0] = stats[2 * col[n][0]], st[n][1] = stats[2 * col[n][1]];
 #pragma unroll
+        for (int i = 0; i < 4; ++i) zp[i] = PRECISE ? ((uint32_t)zr[16 * SUB * i + (SUB == 1 ? 0 : t)] & ((1u << BITS) - 1u)) * 0x10001u : 0u;
+#pragma unroll
         for (int s = 0; s < SUB; ++s) {
           float z[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = -(float)zr[16 * SUB * i + s];
+          for (int i = 0; i < 4; ++i) z[i] = PRECISE ? 0.0f : -(float)zr[16 * SUB * i + s];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (n > 0 && 8 * n >= count) break;
-            const float x0 = SUB == 1 ? st[n][0].y : unit_sums[8 * col[n][0] + s];
-            const float x1 = SUB == 1 ? st[n][1].y : unit_sums[8 * col[n][1] + s];
+            const float x0 = PRECISE ? 0.0f : (SUB == 1 ? st[n][0].y : unit_sums[8 * col[n][0] + s]);
+            const float x1 = PRECISE ? 0.0f : (SUB == 1 ? st[n][1].y : unit_sums[8 * col[n][1] + s]);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              sum[n][s][m][0] = z[2 * m] * x0, sum[n][s][m][1] = z[2 * m] * x1;
-              sum[n][s][m][2] = z[2 * m + 1] * x0, sum[n][s][m][3] = z[2 * m + 1] * x1;
+              sum[n][s][m][0] = PRECISE ? 0.0f : z[2 * m] * x0, sum[n][s][m][1] = PRECISE ? 0.0f : z[2 * m] * x1;
+              sum[n][s][m][2] = PRECISE ? 0.0f : z[2 * m + 1] * x0, sum[n][s][m][3] = PRECISE ? 0.0f : z[2 * m + 1] * x1;
             }
           }
         }
@@ -748,7 +765,13 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
         for (int q = 0; q < 4; ++q) {  // registers 4 q .. 4 q + 3 of the units: 32 of the chunk's columns
           uint32_t v[4][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) unit_quad<BITS>(w[i], q, v[i]);
+          for (int i = 0; i < 4; ++i) {
+            unit_quad<BITS>(w[i], q, v[i]);
+            if constexpr (PRECISE) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[i][j] = less_zero(v[i][j], zp[i] << Pairs<BITS>::p(4 * q + j));
+            }
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (n > 0 && 8 * n >= count) break;
@@ -809,7 +832,7 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
         v += sums[w][r][n];
         if (gated) up += sums[w][16 + r][n];
       }
-      v *= kCodeInverse, up *= kCodeInverse;  // codes were taken as q 2^-24
+      if (!PRECISE) v *= kCodeInverse, up *= kCodeInverse;  // codes were taken as q 2^-24
       if (gated)
         v = v / (1.0f + expf(-v)) * up;
       else if (a.mode == kUpRelu)
@@ -870,7 +893,7 @@ int choose_k_warps(const ProductArgs& a, int tiles, int slots, int* smem) {
   return best;
 }
 
-template <int BITS, int TERMS, int NT, int SUB>
+template <int BITS, int TERMS, int NT, int SUB, bool PRECISE>
 gptq_status launch_product_form(ProductArgs a, int tiles, int sms, cudaStream_t s) {
   const int slots = kCtasPerSm * sms;
   int smem = 0;
@@ -881,18 +904,28 @@ gptq_status launch_product_form(ProductArgs a, int tiles, int sms, cudaStream_t 
   a.k_warps = choose_k_warps<BITS, TERMS, NT, SUB>(a, tiles, slots, &smem);
   const int groups = kProductWarps / a.k_warps;
   const int64_t items = (int64_t)tiles * ((a.row_tiles + groups - 1) / groups);
-  auto kernel = moe_product_kernel<BITS, TERMS, NT, SUB>;
+  auto kernel = moe_product_kernel<BITS, TERMS, NT, SUB, PRECISE>;
   GPTQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   GPTQ_CUDA_TRY(launch_chained(kernel, (unsigned)std::min<int64_t>(items, slots), kProductWarps * 32, smem, s, a));
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
-template <int BITS, int TERMS>
-gptq_status launch_product(const ProductArgs& a, int nt, bool sub, int tiles, int sms, cudaStream_t s) {
-  if (sub) return launch_product_form<BITS, TERMS, 1, 4>(a, tiles, sms, s);
-  return nt == 1 ? launch_product_form<BITS, TERMS, 1, 1>(a, tiles, sms, s)
-                 : launch_product_form<BITS, TERMS, 2, 1>(a, tiles, sms, s);
+template <int BITS, int TERMS, bool PRECISE>
+gptq_status launch_product_typed(const ProductArgs& a, int nt, bool sub, int tiles, int sms, cudaStream_t s) {
+  if (sub) return launch_product_form<BITS, TERMS, 1, 4, PRECISE>(a, tiles, sms, s);
+  return nt == 1 ? launch_product_form<BITS, TERMS, 1, 1, PRECISE>(a, tiles, sms, s)
+                 : launch_product_form<BITS, TERMS, 2, 1, PRECISE>(a, tiles, sms, s);
+}
+
+template <int BITS>
+gptq_status launch_product(bool two_terms, bool precise, const ProductArgs& a, int nt, bool sub, int tiles, int sms,
+                           cudaStream_t s) {
+  if (precise)
+    return two_terms ? launch_product_typed<BITS, 2, true>(a, nt, sub, tiles, sms, s)
+                     : launch_product_typed<BITS, 1, true>(a, nt, sub, tiles, sms, s);
+  return two_terms ? launch_product_typed<BITS, 2, false>(a, nt, sub, tiles, sms, s)
+                   : launch_product_typed<BITS, 1, false>(a, nt, sub, tiles, sms, s);
 }
 
 template <typename T, int BITS, int TERMS>
@@ -920,7 +953,7 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   const int tokens = (int)m.tokens, d = (int)m.d, f = (int)m.f;
   const int pairs = tokens * m.top_k;
   const Terms x_terms = terms_at(ws + l.x_terms, tokens, d), a_terms = terms_at(ws + l.a_terms, pairs, f);
-  const bool x_wide = m.x_dtype == GPTQ_FP32, a_wide = m.y_dtype != GPTQ_BF16;
+  const bool x_wide = m.x_dtype == GPTQ_FP32, a_wide = m.y_dtype != GPTQ_BF16, precise = m.y_dtype == GPTQ_FP32;
   gptq_status st;
   switch (m.x_dtype) {
     case GPTQ_BF16: st = launch_router<__nv_bfloat16, BITS, 1>(m, logits, x_terms, s); break;
@@ -955,7 +988,7 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   a.terms = x_terms;
   a.lists = lists;
   a.out = acts;
-  st = x_wide ? launch_product<BITS, 2>(a, nt, sub, tiles, sms, s) : launch_product<BITS, 1>(a, nt, sub, tiles, sms, s);
+  st = launch_product<BITS>(x_wide, precise, a, nt, sub, tiles, sms, s);
   if (st != GPTQ_OK) return st;
   const unsigned layout_blocks = (unsigned)(((int64_t)pairs * a_terms.chunks * 4 + 255) / 256);
   if (a_wide)
@@ -971,7 +1004,7 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   a.spans = a_terms.chunks / 2, a.row_tiles = d / 32;
   a.terms = a_terms;
   a.out = products;
-  st = a_wide ? launch_product<BITS, 2>(a, nt, sub, tiles, sms, s) : launch_product<BITS, 1>(a, nt, sub, tiles, sms, s);
+  st = launch_product<BITS>(a_wide, precise, a, nt, sub, tiles, sms, s);
   if (st != GPTQ_OK) return st;
   const unsigned blocks = (unsigned)(((int64_t)tokens * d + 255) / 256);
   switch (m.y_dtype) {

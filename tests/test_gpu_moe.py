@@ -76,12 +76,22 @@ class Case:
         chunks of 128 columns and 8 warps: 2 + chunks + 8.  x itself: 2^-24 of each value where it takes two terms
         (fp32), exact where one holds it, and in both 2^-32 of the block's largest for values too small for fp16.
         silu's slope is below 1.1 and its own evaluation a few u; the intermediate takes two terms (2^-24 of each value),
-        or one for a bf16 result (2^-12)."""
+        or one for a bf16 result (2^-12).
+        For a 16-bit result the codes are fp16 subnormals q 2^(p - 24), which the tensor core aligns as if they were 2^-14:
+        each of the 17 additions of the 8 steps of at most two terms may be off by 2^-24 of 2^-13 times the block's largest
+        |x|, in units of the code (2^-24) and with 2^-p <= 1: 272 * 2^-13 s max|x| per block of 128."""
 
-        def product(W, A, v, ev, own):  # W v with |v's error| <= ev; own: v's rounding to its terms
+        def product(W, A, scales, v, ev, own):  # W v with |v's error| <= ev; own: v's rounding to its terms
             n = 544 + 36 + 10 + -(-v.numel() // 128)
             ev = ev + own * v.abs() + 2.0 ** -32 * v.abs().max()
-            return W @ v, n * U * (A @ v.abs()) + A @ ev
+            tol = n * U * (A @ v.abs()) + A @ ev
+            if self.ydt != torch.float32:
+                s = scales.double().repeat_interleave(self.gs or v.numel(), -1)
+                pad = (0, -v.numel() % 128)
+                s = torch.nn.functional.pad(s, pad).view(s.shape[0], -1, 128).amax(-1)
+                big = torch.nn.functional.pad(v.abs() + ev, pad).view(-1, 128).amax(-1)
+                tol = tol + 272 * 2.0 ** -13 * (s @ big)
+            return W @ v, tol
 
         x, ids, w = self.x.double(), self.ids.long(), self.w.double()
         xown = 2.0 ** -24 if self.x.dtype == torch.float32 else 0.0
@@ -92,15 +102,15 @@ class Case:
                 e = int(ids[t, k])
                 if not 0 <= e < self.e:
                     continue
-                u, eu = product(self.Wu[e], self.Au[e], x[t], 0.0, xown)
+                u, eu = product(self.Wu[e], self.Au[e], self.up[1][e], x[t], 0.0, xown)
                 if self.act == g.GPTQ_ACT_SILU_GATED:
-                    z, ez = product(self.Wg[e], self.Ag[e], x[t], 0.0, xown)
+                    z, ez = product(self.Wg[e], self.Ag[e], self.gate[1][e], x[t], 0.0, xown)
                     sl = z * torch.sigmoid(z)
                     h = sl * u
                     eh = 1.1 * ez * (u.abs() + eu) + sl.abs() * eu + 16 * U * h.abs()
                 else:
                     h, eh = torch.relu(u), eu
-                v, ev = product(self.Wd[e], self.Ad[e], h, eh, hown)
+                v, ev = product(self.Wd[e], self.Ad[e], self.down[1][e], h, eh, hown)
                 y[t] += w[t, k] * v
                 tol[t] += w[t, k] * (ev + (2 + self.top) * U * v.abs())
         if self.ydt != torch.float32:
