@@ -286,7 +286,8 @@ GPTQ_API gptq_status gptq_dequantize(const int32_t* packed, const float* scales,
  *   smallest integer e >= -126 with a <= 448 * 2^e, and s = 1 when a = 0.  A division by a power of
  *   two is exact, so rounding to e4m3 (to nearest, ties to even) is the only rounding.  NaN and
  *   infinite values become the NaN code and leave the scale alone.
- *   X          [m, k] row-major, BF16 / FP16 / FP32, 16-byte aligned; k % 16 == 0; m may be 0.
+ *   X          [m, k] row-major, BF16 / FP16 / FP32, 16-byte aligned; k % 16 == 0, k <= 2^20; m may be 0,
+ *              m <= 2^26 (with block_rows 128: fewer than 2^31 blocks).
  *   Q          [m, k] e4m3 output, 16-byte aligned; must not overlap X.
  *   scales     [ceil(m / block_rows), ceil(k / 128)] fp32 output.
  *

@@ -55,7 +55,7 @@ struct Args {
   int tiles_t, tiles_w, units;     // token tiles, weight tiles, work units
   int kb_per_split;
   int scale_width;                 // floats per load that the scales' rows are aligned for: 1, 2 or 4
-  bool vec_y;                      // 16-byte accesses to Y's rows are aligned
+  bool vec_y, pair_y;              // Y's rows start on 16 bytes, on pairs of values
   int token_bytes;                 // bytes of a stage's token box (fewer than 128 rows when m is small)
   uint32_t idesc;
   const float* a_scales;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
         }
       }
       if (ok && rows_here) {
-        const bool even = a.partial || (a.n & 1) == 0;  // rows start on pairs
+        const bool even = a.partial || a.pair_y;  // rows start on pairs
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tok = t0 + 32 * quad + r4 + 8 * i;
@@ -755,7 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         if (row0 + lane < a.m && w0 < a.n)
           store_row<128>(acc, static_cast<TY*>(a.Y) + (int64_t)(row0 + lane) * a.n + w0, a.n - w0);
       } else {
-        const bool even = (a.n & 1) == 0;  // rows start on pairs
+        const bool even = a.pair_y;  // rows start on pairs
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tok = row0 + rr + 8 * i, w = w0 + cc;
@@ -1084,7 +1084,9 @@ gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* 
   while (a.scale_width > 1 && (p.kb % a.scale_width || !aligned(a_scales, 4 * a.scale_width) ||
                                !aligned(b_scales, 4 * a.scale_width)))
     a.scale_width /= 2;
-  a.vec_y = n * (y_dtype == GPTQ_FP32 ? 4 : 2) % 16 == 0 && aligned(Y, 16);
+  const int y_size = y_dtype == GPTQ_FP32 ? 4 : 2;
+  a.vec_y = n * y_size % 16 == 0 && aligned(Y, 16);
+  a.pair_y = n % 2 == 0 && aligned(Y, 2 * y_size);
   const bool block = b_block_rows == 128;
   a.a_scales = a_scales, a.b_scales = b_scales;
   a.Y = Y;

@@ -314,10 +314,9 @@ __global__ void __launch_bounds__(kThreads) fp8_from_packed_kernel(const uint32_
 template <typename T>
 gptq_status quantize_typed(const T* X, int64_t m, int k, int block_rows, uint8_t* Q, float* scales, cudaStream_t s) {
   const int kb = (k + kBlockCols - 1) / kBlockCols;
-  if (block_rows == 1 && k % kBlockCols == 0) {
-    const int64_t granules = m * (k / 8), blocks = (granules + kThreads * kInFlight - 1) / (kThreads * kInFlight);
-    if (blocks > 0x7fffffff) return GPTQ_ERR_ARG;
-    fp8_quantize_linear_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(X, granules, Q, scales);
+  const int64_t granules = m * (k / 8), linear_blocks = (granules + kThreads * kInFlight - 1) / (kThreads * kInFlight);
+  if (block_rows == 1 && k % kBlockCols == 0 && linear_blocks <= 0x7fffffff) {
+    fp8_quantize_linear_kernel<T><<<(unsigned)linear_blocks, kThreads, 0, s>>>(X, granules, Q, scales);
   } else if (block_rows == 1) {
     int per_row = 16;
     while (per_row < kThreads && per_row < kb * 16) per_row *= 2;

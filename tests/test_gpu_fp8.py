@@ -171,6 +171,33 @@ def test_matmul_is_deterministic_and_keeps_to_its_rows():
         assert torch.equal(t, b)
 
 
+@pytest.mark.parametrize("m,n,k", [(9, 1, 16), (300, 3, 48), (130, 200, 16), (300, 40, 128), (4, 2, 16)])
+def test_small_matrices(m, n, k):
+    """Boxes larger than the matrices they are cut from, in every form."""
+    A, sa, B, sb = _operands(m, n, k, 1, m + n, S.dev())
+    _check_matmul(_matmul(A, sa, B, sb, 1, torch.float32), A, sa, B, sb, 1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(5, 64, 256), (40, 64, 256), (300, 256, 256), (300, 512, 4224)])
+def test_outputs_and_scales_on_any_alignment(m, n, k, dtype):
+    """Y, the scales and the status as views that start one value into their memory."""
+    dev = S.dev()
+    A, sa, B, sb = _operands(m, n, k, 1, 3, dev)
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device=dev)
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+
+    Y = shifted(torch.full((m, n), float("nan"), dtype=dtype, device=dev))
+    sa, sb, st = shifted(sa), shifted(sb), shifted(torch.zeros(2, dtype=torch.int32, device=dev))
+    ws = torch.empty(max(256, g.gptq_fp8_matmul_workspace_size(m, n, k)), dtype=torch.uint8, device=dev)
+    g.gptq_fp8_matmul(A, sa, B, sb, 1, Y, st, ws)
+    assert g.gptq_read_status(st)[0] == g.GPTQ_OK
+    _check_matmul(Y, A, sa, B, sb, 1)
+
+
 def test_nan_stays_in_its_row_and_column():
     m, n, k = 40, 200, 512
     A, sa, B, sb = _operands(m, n, k, 1, 9, S.dev())

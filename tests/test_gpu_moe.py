@@ -214,6 +214,26 @@ def test_large_values_do_not_overflow_early():
     c.check()
 
 
+@pytest.mark.parametrize("bits,gs", [(4, 128), (3, 128), (2, 32), (3, 0)])
+def test_grids_and_outputs_on_any_alignment(bits, gs):
+    """Scales, zeros, routing, Y and status as views that start one value into their memory."""
+    c = Case(3, 4, 2, 256, 256, bits, gs, bf, hf, SILU)
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device=t.device)
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+
+    for name in ("up", "gate", "down"):
+        w = getattr(c, name)
+        setattr(c, name, (w[0], shifted(w[1]), shifted(w[2])))
+    c.ids, c.w, c.Y, c.st = shifted(c.ids), shifted(c.w), shifted(c.Y), shifted(c.st)
+    c.run()
+    assert g.gptq_read_status(c.st)[0] == g.GPTQ_OK
+    c.check_routing(False)
+    c.check()
+
+
 def test_no_tokens_is_no_work():
     c = Case(1, 2, 1, 64, 32, 4, 0, bf, ff, RELU)
     n0 = g.gptq_kernel_launches()
