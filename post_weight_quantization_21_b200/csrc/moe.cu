@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
   const int steps = a.spans > kw ? (a.spans - kw + a.k_warps - 1) / a.k_warps : 0;  // this group's spans
 
   // ---- the copies: span after span of item after item
-  const int gt = rg * 32 + lane, gn = groups * 32;  // this thread among its group's
+  const int gt = rg * 32 + lane;  // this thread among its group's
   // an item is row tiles in_rt .. of list tile in_tile; the next one lies gridDim.x items further on
   const int hop_tile = (int)gridDim.x / per_tile, hop_rt = (int)gridDim.x % per_tile;
   auto hop = [&](int& tile, int& rt) {
@@ -573,8 +573,8 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
   const uint32_t *words0 = nullptr, *words1 = nullptr;  // span in_c of the M tiles' first rows
   const float* scales = nullptr;       // row `lane` of the tile
   const int32_t* zeros = nullptr;
-  const uint16_t* token_src = nullptr;  // this thread's first piece of the tokens' terms, and of their sums
-  const float2* stat_src = nullptr;
+  const char* term0 = reinterpret_cast<const char*>(a.terms.values) + lane * 16;
+  const char* term1 = term0 + 2 * a.terms.stride;
   // This lane's 16-byte pieces of an M tile's codes: piece p = lane + 32 i is piece p % PP of row p / PP.  From
   // the tile's first row to them, in words and in bytes of the stage:
   constexpr int PP = 2 * BITS, NI = 16 * PP / 32;
@@ -599,10 +599,6 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
     const int64_t lane_row = (r + (gated ? lane & 15 : lane)) * a.ng;
     scales = (gated && lane >= 16 ? a.b.scales : a.a.scales) + lane_row;
     zeros = (gated && lane >= 16 ? a.b.zeros : a.a.zeros) + lane_row;
-    const int j = gt / (32 * TERMS), k = gt / 32 % TERMS;
-    if (j < in_count)
-      token_src = a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.terms.chunks + 2 * kw) * 128 + (gt & 31) * 8;
-    if (gt < in_count) stat_src = a.terms.chunk + ((int64_t)row_of[in_first + gt] * a.terms.chunks + 2 * kw);
   };
   auto issue = [&]() {
     if (in_tile < n_tiles && steps > 0) {
@@ -636,30 +632,26 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
           copy_async<4>(grids + (32 * 2 * SUB + s) * 4, zeros + grid);
         }
       }
-      // the group's threads share its tokens: 32 pieces per token and term, odd tokens' neighbouring quads exchanged
-      // so that two tokens' pieces of one quad lie in different banks
+      // the group's warps share its tokens: 32 pieces per token and term, odd tokens' neighbouring quads exchanged
+      // so that two tokens' pieces of one quad lie in different banks.  (Offsets from a term's start fit 32 bits: at
+      // most 1024 rows of 8192 chunks of 256 bytes.)
       const uint32_t tokens = stage + my_tokens;
-      const int pieces = in_count * (32 * TERMS);
-      if (gt < pieces)
-        copy_async<16>(tokens + (gt >> 5) * 512 + ((gt & 31) ^ 4 * (gt / (32 * TERMS) & 1)) * 16, token_src);
-      for (int p = gt + gn; p < pieces; p += gn) {
-        const int j = p / (32 * TERMS), k = p / 32 % TERMS;
-        copy_async<16>(tokens + (p >> 5) * 512 + ((p & 31) ^ 4 * (j & 1)) * 16,
-                       a.terms.values + k * a.terms.stride + ((int64_t)row_of[in_first + j] * a.terms.chunks + 2 * c) * 128 + (p & 31) * 8);
+      for (int i = rg; i < in_count * TERMS; i += groups) {
+        const int j = TERMS == 1 ? i : i >> 1;
+        const uint32_t at = (uint32_t)row_of[in_first + j] * (uint32_t)a.terms.chunks + 2u * (uint32_t)c;
+        copy_async<16>(tokens + i * 512 + (lane ^ 4 * (j & 1)) * 16, (TERMS > 1 && (i & 1) ? term1 : term0) + (at << 8));
       }
-      const uint32_t stats = tokens + a.cols * (TERMS * 512);
       if (gt < in_count) {  // at most 16 tokens: the group's first warp
-        copy_async<16>(stats + gt * 16, stat_src);
-        if constexpr (SUB > 1) {
-          const float* units = a.terms.unit + (stat_src - a.terms.chunk) * 4;
-          copy_async<16>(stats + a.cols * 16 + gt * 32, units);
-          copy_async<16>(stats + a.cols * 16 + gt * 32 + 16, units + 4);
+        const uint32_t stats = tokens + a.cols * (TERMS * 512);
+        const uint32_t at = (uint32_t)row_of[in_first + gt] * (uint32_t)a.terms.chunks + 2u * (uint32_t)c;
+        copy_async<16>(stats + gt * 16, a.terms.chunk + at);
+        if constexpr (SUB > 1 && !PRECISE) {
+          copy_async<16>(stats + a.cols * 16 + gt * 32, a.terms.unit + at * 4);
+          copy_async<16>(stats + a.cols * 16 + gt * 32 + 16, a.terms.unit + at * 4 + 4);
         }
       }
       in_c += a.k_warps;
       words0 += a.k_warps * (8 * BITS), words1 += a.k_warps * (8 * BITS);
-      token_src += a.k_warps * 256;
-      stat_src += a.k_warps * 2;
       if (in_c >= a.spans) {
         in_c = kw;
         hop(in_tile, in_rt);
@@ -705,7 +697,7 @@ __global__ void __launch_bounds__(kProductWarps * 32, kCtasPerSm) moe_product_ke
       if (groups == 1)
         __syncwarp();
       else
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "r"(gn) : "memory");
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "r"(groups * 32) : "memory");
       issue();
       const uint8_t* stage = ring + out_stage;
       out_stage += stage_bytes;
