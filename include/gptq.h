@@ -354,8 +354,12 @@ GPTQ_API size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  *   router top_k <= 16); bits in {2, 3, 4}; group_size 0 or a multiple of 32 that divides d and f.
  *   Under act-order the packed codes are in the quantization order and X's (and a_i's) columns have to be
  *   permuted alike, which this call does not do.
- * Products q x are exact (X is split into bf16 terms that add up to it; a_i stays in fp32 and is split into three,
- * or into two where Y has 16 bits), sums fp32 and in a fixed order: results are deterministic.
+ * The weights enter the products as the integers q - zero (or q, the zero points apart), exactly.  Values enter as
+ * fp16 terms of x * 2^-e, one e per token and 128 columns: one term for 16-bit X (exact down to 2^-21 of the
+ * block's largest value, off by less than 2^-32 of that below it), two for FP32 X (2^-24 of the value); a_i, an fp32 number,
+ * takes two terms, or one (2^-12) where Y is BF16.  Sums are fp32 and in a fixed order: results are
+ * deterministic.  With a 16-bit Y the tensor cores' sums over 128 columns are off by up to 4e-5 of the
+ * products' magnitude, a tenth of Y's own rounding and less; with an FP32 Y they are not (about 1e-6).
  * ------------------------------------------------------------------------------------------ */
 #define GPTQ_ACT_SILU_GATED 0
 #define GPTQ_ACT_RELU 1
