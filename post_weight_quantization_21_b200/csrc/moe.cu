@@ -955,7 +955,7 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   if (st != GPTQ_OK) return st;
   // An expert's list goes 8 tokens at a time, or 16 where lists are long (more than 12 on average), so that the
   // codes are taken apart once for two N tiles; 16 tokens' terms leave fewer groups room, so for short lists they
-  // only cost (32 tokens, 6 of 32 experts each: 196 us with 16 at a time, 152 with 8).  Scales that change inside
+  // only cost (32 tokens, 6 of 32 experts each: 214 us with 16 at a time, 173 with 8).  Scales that change inside
   // a chunk need the registers of the second N tile.
   const bool sub = m.group_size == 32 || m.group_size == 64;
   const int nt = pairs <= 12 * m.experts || sub ? 1 : 2;
