@@ -350,13 +350,13 @@ __device__ __forceinline__ uint32_t ordered(float v) {  // larger float <=> larg
 }
 
 // One CTA.  A warp per token chooses its experts (largest logits first, ties to the lowest index) and their
-// weights; then every expert's thread collects its pairs in order.
+// weights; then a warp per expert collects its pairs in order.
 __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict__ logits, int tokens, int experts,
                                                          int top_k, int renormalize, int tile_tokens,
                                                          int32_t* __restrict__ ids, float* __restrict__ weights,
                                                          Lists* __restrict__ lists, int32_t* status) {
   __shared__ int32_t id_of[kMaxPairs];
-  __shared__ int32_t first_of[kMaxExperts], tile_of[kMaxExperts];
+  __shared__ int32_t first_of[kMaxExperts], count_of[kMaxExperts], tile_of[kMaxExperts];
   wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = tokens * top_k;
@@ -414,12 +414,10 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict
     }
   }
   __syncthreads();
-  const int e = threadIdx.x;
-  int count = 0;
-  if (e < experts) {
-    for (int p = 0; p < pairs; ++p) count += id_of[p] == e;
-    first_of[e] = count;
-    tile_of[e] = (count + tile_tokens - 1) / tile_tokens;
+  for (int e = warp; e < experts; e += 32) {
+    int count = 0;
+    for (int p = lane; p - lane < pairs; p += 32) count += __popc(__ballot_sync(0xffffffffu, p < pairs && id_of[p] == e));
+    if (lane == 0) first_of[e] = count_of[e] = count, tile_of[e] = (count + tile_tokens - 1) / tile_tokens;
   }
   __syncthreads();
   if (warp == 0) {  // exclusive sums over the experts, 32 at a time
@@ -442,12 +440,17 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict
     if (lane == 0) lists->n_tiles = tile_base;
   }
   __syncthreads();
-  if (e < experts && count > 0) {
+  for (int e = warp; e < experts; e += 32) {
     int at = first_of[e];
-    for (int p = 0; p < pairs; ++p)
-      if (id_of[p] == e) lists->pairs[at++] = p;
-    for (int i = 0, left = count; left > 0; ++i, left -= tile_tokens)
-      lists->tiles[tile_of[e] + i] = {e, first_of[e] + i * tile_tokens, min(left, tile_tokens)};
+    const int count = count_of[e];
+    for (int i = lane; i * tile_tokens < count; i += 32)
+      lists->tiles[tile_of[e] + i] = {e, at + i * tile_tokens, min(count - i * tile_tokens, tile_tokens)};
+    for (int p = lane; p - lane < pairs; p += 32) {
+      const bool mine = p < pairs && id_of[p] == e;
+      const uint32_t all = __ballot_sync(0xffffffffu, mine);
+      if (mine) lists->pairs[at + __popc(all & ((1u << lane) - 1u))] = p;
+      at += __popc(all);
+    }
   }
 }
 
