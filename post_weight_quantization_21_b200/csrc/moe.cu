@@ -23,7 +23,8 @@
 // takes two terms, or one where Y is bf16 (2^-12 beside the result's own 2^-9).  Products are then exact in
 // the tensor core, sums run there over 128 columns and in fp32 beyond.
 //
-// Launches: router logits and the tokens' layout; top-K and the lists of tokens per expert; the up product
+// Launches: router logits and the tokens' layout; top-K and the lists of tokens per expert (one launch with the
+// router where there are few logits); the up product
 // with the activation; the activations' layout; the down product; the weighted sum in the order of the choice.
 // No atomics: results are deterministic.
 #include <algorithm>
@@ -281,53 +282,64 @@ __device__ __forceinline__ void layout_unit(const T* __restrict__ row, int64_t r
 
 constexpr int kRouterTokens = 8;  // tokens per CTA of the logits
 
-// CTAs [0, experts * token groups): logits of one expert for up to 8 tokens.  The others: the tokens' layout, a
-// thread per unit of 32 columns.
+// Logits of one expert for up to 8 tokens, by a CTA of 256 threads: item = token group * experts + expert.
+template <typename T>
+__device__ __forceinline__ void router_logits(const T* __restrict__ X, const T* __restrict__ R, int tokens, int d,
+                                              int experts, int item, float* logits) {
+  const int e = item % experts, t0 = item / experts * kRouterTokens;
+  const int nt = min(kRouterTokens, tokens - t0);
+  float acc[kRouterTokens];
+#pragma unroll
+  for (int t = 0; t < kRouterTokens; ++t) acc[t] = 0.0f;
+  for (int c = threadIdx.x * 8; c < d; c += 256 * 8) {
+    float r[8];
+    load8<T>(R + (int64_t)e * d + c, r);
+#pragma unroll
+    for (int t = 0; t < kRouterTokens; ++t) {
+      if (t < nt) {
+        float x[8];
+        load8<T>(X + (int64_t)(t0 + t) * d + c, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[t] = fmaf(x[i], r[i], acc[t]);
+      }
+    }
+  }
+  __shared__ float part[8][kRouterTokens];
+#pragma unroll
+  for (int t = 0; t < kRouterTokens; ++t) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][t] = acc[t];
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < nt) {
+    float s = 0.0f;
+    for (int w = 0; w < 8; ++w) s += part[w][threadIdx.x];
+    logits[(int64_t)(t0 + threadIdx.x) * experts + e] = s;
+  }
+}
+
+// The layout of rows of values, a thread per unit of 32 columns: thread i of them all.
+template <typename T, int BITS, int TERMS>
+__device__ __forceinline__ void layout_thread(const T* __restrict__ X, int64_t rows, int cols, int64_t i,
+                                              const Terms& terms) {
+  const int per_row = terms.chunks * 4;
+  const int64_t n = rows * per_row;
+  const int64_t r = min(i, n - 1) / per_row;  // past the end: the last chunk once more (whole warps shuffle)
+  const int u = (int)(i < n ? i - r * per_row : per_row - 4 + (i & 3));
+  layout_unit<T, BITS, TERMS>(X + r * cols, r, u, cols >> 5, terms);
+}
+
+// CTAs [0, experts * token groups): an item of the logits each.  The others: the tokens' layout.
 template <typename T, int BITS, int TERMS>
 __global__ void __launch_bounds__(256) moe_router_kernel(const T* __restrict__ X, const T* __restrict__ R, int tokens,
                                                          int d, int experts, int router_blocks,
                                                          float* __restrict__ logits, const Terms terms) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if ((int)blockIdx.x < router_blocks) {
-    const int e = blockIdx.x % experts, t0 = blockIdx.x / experts * kRouterTokens;
-    const int nt = min(kRouterTokens, tokens - t0);
-    float acc[kRouterTokens];
-#pragma unroll
-    for (int t = 0; t < kRouterTokens; ++t) acc[t] = 0.0f;
-    for (int c = threadIdx.x * 8; c < d; c += 256 * 8) {
-      float r[8];
-      load8<T>(R + (int64_t)e * d + c, r);
-#pragma unroll
-      for (int t = 0; t < kRouterTokens; ++t) {
-        if (t < nt) {
-          float x[8];
-          load8<T>(X + (int64_t)(t0 + t) * d + c, x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[t] = fmaf(x[i], r[i], acc[t]);
-        }
-      }
-    }
-    __shared__ float part[8][kRouterTokens];
-#pragma unroll
-    for (int t = 0; t < kRouterTokens; ++t) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][t] = acc[t];
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < nt) {
-      float s = 0.0f;
-      for (int w = 0; w < 8; ++w) s += part[w][threadIdx.x];
-      logits[(int64_t)(t0 + threadIdx.x) * experts + e] = s;
-    }
-    return;
-  }
-  const int per_row = terms.chunks * 4;
-  const int64_t n = (int64_t)tokens * per_row;
-  const int64_t i = (int64_t)(blockIdx.x - router_blocks) * 256 + threadIdx.x;
-  const int64_t r = min(i, n - 1) / per_row;  // past the end: the last chunk once more (whole warps shuffle)
-  const int u = (int)(i < n ? i - r * per_row : per_row - 4 + (i & 3));
-  layout_unit<T, BITS, TERMS>(X + r * d, r, u, d >> 5, terms);
+  if ((int)blockIdx.x < router_blocks)
+    router_logits<T>(X, R, tokens, d, experts, blockIdx.x, logits);
+  else
+    layout_thread<T, BITS, TERMS>(X, tokens, d, (int64_t)(blockIdx.x - router_blocks) * 256 + threadIdx.x, terms);
 }
 
 // the activations' layout
@@ -335,12 +347,7 @@ template <int BITS, int TERMS>
 __global__ void __launch_bounds__(256) moe_layout_kernel(const float* __restrict__ acts, int64_t rows, int cols,
                                                          const Terms terms) {
   wait_for_previous();
-  const int per_row = terms.chunks * 4;
-  const int64_t n = rows * per_row;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = min(i, n - 1) / per_row;
-  const int u = (int)(i < n ? i - r * per_row : per_row - 4 + (i & 3));
-  layout_unit<float, BITS, TERMS>(acts + r * cols, r, u, cols >> 5, terms);
+  layout_thread<float, BITS, TERMS>(acts, rows, cols, (int64_t)blockIdx.x * 256 + threadIdx.x, terms);
 }
 
 // ------------------------------------------------------------------ top-K and the lists
@@ -349,19 +356,26 @@ __device__ __forceinline__ uint32_t ordered(float v) {  // larger float <=> larg
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One CTA.  A warp per token chooses its experts (largest logits first, ties to the lowest index) and their
-// weights; then a warp per expert collects its pairs in order.
-__global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict__ logits, int tokens, int experts,
-                                                         int top_k, int renormalize, int tile_tokens,
-                                                         int32_t* __restrict__ ids, float* __restrict__ weights,
-                                                         Lists* __restrict__ lists, int32_t* status) {
+// By one CTA of WARPS warps.  A warp per token chooses its experts (largest logits first, ties to the lowest index) and
+// their weights; then a warp per expert collects its pairs in order.
+struct Route {
+  int tokens, experts, top_k, renormalize, tile_tokens;
+  int32_t* ids;
+  float* weights;
+  Lists* lists;
+  int32_t* status;
+};
+template <int WARPS>
+__device__ __forceinline__ void route(const float* logits, const Route& a) {
   __shared__ int32_t id_of[kMaxPairs];
   __shared__ int32_t first_of[kMaxExperts], count_of[kMaxExperts], tile_of[kMaxExperts];
-  wait_for_previous();
+  const int tokens = a.tokens, experts = a.experts, top_k = a.top_k, tile_tokens = a.tile_tokens;
+  int32_t* ids = a.ids;
+  Lists* lists = a.lists;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = tokens * top_k;
   if (logits != nullptr) {
-    for (int t = warp; t < tokens; t += 32) {
+    for (int t = warp; t < tokens; t += WARPS) {
       constexpr int N = kMaxExperts / 32;
       float l[N];
       uint32_t key[N];
@@ -369,7 +383,7 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int e = lane + 32 * i;
-        l[i] = e < experts ? logits[(int64_t)t * experts + e] : -INFINITY;
+        l[i] = e < experts ? __ldcg(logits + t * experts + e) : -INFINITY;
         key[i] = e < experts ? max(ordered(l[i]), 1u) : 0u;  // 0: not there, or chosen before
         mx = fmaxf(mx, l[i]);
       }
@@ -404,17 +418,17 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict
           id_of[t * top_k + k] = e;
         }
       }
-      if (lane < top_k) weights[t * top_k + lane] = renormalize ? mine / chosen : mine;
+      if (lane < top_k) a.weights[t * top_k + lane] = a.renormalize ? mine / chosen : mine;
     }
   } else {
-    for (int p = threadIdx.x; p < pairs; p += 1024) {
+    for (int p = threadIdx.x; p < pairs; p += 32 * WARPS) {
       const int e = ids[p];
-      if (e < 0 || e >= experts) report_status(status, GPTQ_ERR_ARG, p);
+      if (e < 0 || e >= experts) report_status(a.status, GPTQ_ERR_ARG, p);
       id_of[p] = e;
     }
   }
   __syncthreads();
-  for (int e = warp; e < experts; e += 32) {
+  for (int e = warp; e < experts; e += WARPS) {
     int count = 0;
     for (int p = lane; p - lane < pairs; p += 32) count += __popc(__ballot_sync(0xffffffffu, p < pairs && id_of[p] == e));
     if (lane == 0) first_of[e] = count_of[e] = count, tile_of[e] = (count + tile_tokens - 1) / tile_tokens;
@@ -440,7 +454,7 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict
     if (lane == 0) lists->n_tiles = tile_base;
   }
   __syncthreads();
-  for (int e = warp; e < experts; e += 32) {
+  for (int e = warp; e < experts; e += WARPS) {
     int at = first_of[e];
     const int count = count_of[e];
     for (int i = lane; i * tile_tokens < count; i += 32)
@@ -452,6 +466,31 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict
       at += __popc(all);
     }
   }
+}
+
+__global__ void __launch_bounds__(1024) moe_route_kernel(const float* logits, const Route a) {
+  wait_for_previous();
+  route<32>(logits, a);
+}
+
+// Router and choice in one launch, where the logits are at most an item for each CTA of a cluster: when all are there its
+// first CTA chooses.  The other clusters: the tokens' layout.  In a graph the two forms take the same (1 token,
+// 8 experts, d 4096: 17.4 us the layer with f = 256), and the host has one launch less (5 tokens, 4 experts of 768 x 768
+// called from Python: 25.4 -> 22.7 us); with two items a CTA the launch saved is lost again (8 tokens, 16
+// experts: 28.8 -> 33.5).
+constexpr int kRouteCluster = 8;
+template <typename T, int BITS, int TERMS>
+__global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(256)
+    moe_router_route_kernel(const T* __restrict__ X, const T* __restrict__ R, int d, int items, float* logits,
+                            const Terms terms, const Route a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x >= kRouteCluster) {
+    layout_thread<T, BITS, TERMS>(X, a.tokens, d, (int64_t)(blockIdx.x - kRouteCluster) * 256 + threadIdx.x, terms);
+    return;
+  }
+  if ((int)blockIdx.x < items) router_logits<T>(X, R, a.tokens, d, a.experts, blockIdx.x, logits);
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blockIdx.x == 0) route<8>(R != nullptr ? logits : nullptr, a);
 }
 
 // ------------------------------------------------------------------ products with packed weights
@@ -924,12 +963,22 @@ gptq_status launch_product(bool two_terms, bool precise, const ProductArgs& a, i
 }
 
 template <typename T, int BITS, int TERMS>
-gptq_status launch_router(const MoeArgs& m, float* logits, const Terms& terms, cudaStream_t s) {
+gptq_status launch_router(const MoeArgs& m, float* logits, const Terms& terms, const Route& r, cudaStream_t s) {
   const int tokens = (int)m.tokens, d = (int)m.d;
-  const int router_blocks = m.router ? m.experts * ((tokens + kRouterTokens - 1) / kRouterTokens) : 0;
+  const T *X = static_cast<const T*>(m.X), *R = static_cast<const T*>(m.router);
+  const int items = m.experts * ((tokens + kRouterTokens - 1) / kRouterTokens);
   const int layout_blocks = (int)(((int64_t)tokens * terms.chunks * 4 + 255) / 256);
-  moe_router_kernel<T, BITS, TERMS><<<router_blocks + layout_blocks, 256, 0, s>>>(
-      static_cast<const T*>(m.X), static_cast<const T*>(m.router), tokens, d, m.experts, router_blocks, logits, terms);
+  if (items <= kRouteCluster) {
+    const int blocks = kRouteCluster + (layout_blocks + kRouteCluster - 1) / kRouteCluster * kRouteCluster;
+    moe_router_route_kernel<T, BITS, TERMS><<<blocks, 256, 0, s>>>(X, R, d, R ? items : 0, logits, terms, r);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+  }
+  const int router_blocks = R ? items : 0;
+  moe_router_kernel<T, BITS, TERMS><<<router_blocks + layout_blocks, 256, 0, s>>>(X, R, tokens, d, m.experts,
+                                                                                  router_blocks, logits, terms);
+  GPTQ_LAUNCH_CHECK();
+  GPTQ_CUDA_TRY(launch_chained(moe_route_kernel, 1, 1024, 0, s, R ? logits : nullptr, r));
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -949,13 +998,6 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   const int pairs = tokens * m.top_k;
   const Terms x_terms = terms_at(ws + l.x_terms, tokens, d), a_terms = terms_at(ws + l.a_terms, pairs, f);
   const bool x_wide = m.x_dtype == GPTQ_FP32, a_wide = m.y_dtype != GPTQ_BF16, precise = m.y_dtype == GPTQ_FP32;
-  gptq_status st;
-  switch (m.x_dtype) {
-    case GPTQ_BF16: st = launch_router<__nv_bfloat16, BITS, 1>(m, logits, x_terms, s); break;
-    case GPTQ_FP16: st = launch_router<__half, BITS, 1>(m, logits, x_terms, s); break;
-    default: st = launch_router<float, BITS, 2>(m, logits, x_terms, s); break;
-  }
-  if (st != GPTQ_OK) return st;
   // An expert's list goes 8 tokens at a time, or 16 where lists are long (more than 12 on average), so that the
   // codes are taken apart once for two N tiles; 16 tokens' terms leave fewer groups room, so for short lists they
   // only cost (32 tokens, 6 of 32 experts each: 214 us with 16 at a time, 173 with 8).  Scales that change inside
@@ -964,9 +1006,14 @@ gptq_status moe_typed(const MoeArgs& m, cudaStream_t s) {
   const int nt = pairs <= 12 * m.experts || sub ? 1 : 2;
   const int tile_tokens = 8 * nt;
   const int tiles = std::min(pairs, std::min(m.experts, pairs) + pairs / tile_tokens);  // at most
-  GPTQ_CUDA_TRY(launch_chained(moe_route_kernel, 1, 1024, 0, s, m.router ? logits : nullptr, tokens, m.experts, m.top_k,
-                               m.renormalize, tile_tokens, m.ids, m.weights, lists, m.status));
-  GPTQ_LAUNCH_CHECK();
+  const Route r = {tokens, m.experts, m.top_k, m.renormalize, tile_tokens, m.ids, m.weights, lists, m.status};
+  gptq_status st;
+  switch (m.x_dtype) {
+    case GPTQ_BF16: st = launch_router<__nv_bfloat16, BITS, 1>(m, logits, x_terms, r, s); break;
+    case GPTQ_FP16: st = launch_router<__half, BITS, 1>(m, logits, x_terms, r, s); break;
+    default: st = launch_router<float, BITS, 2>(m, logits, x_terms, r, s); break;
+  }
+  if (st != GPTQ_OK) return st;
   ProductArgs a = {};
   a.mode = m.gated ? kUpGated : kUpRelu;
   auto matrix = [](const MoePacked& p) {
