@@ -43,7 +43,8 @@ struct Cfg {
   static constexpr int kStageBytes = (BM + NT) * BK;
   static constexpr int kStages = kSmemBudget / kStageBytes > 10 ? 10 : kSmemBudget / kStageBytes;
   static constexpr int kAccs = 4;  // accumulators in TMEM
-  static constexpr int kTmemCols = NT * kAccs < 32 ? 32 : NT * kAccs;
+  static constexpr int kAccCols = NT == 96 ? 128 : NT;  // from one to the next: TMEM comes in powers of two
+  static constexpr int kTmemCols = kAccCols * kAccs;
   static constexpr int kCols = NT * 4 / kEpiWarps;  // weight rows per epilogue warp
   static constexpr int kScaleRow = BM + NT;  // staged scales per block
   static constexpr int kScaleBytes = 2 * SG * kScaleRow * 4;
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
           const uint64_t wd = td + (uint64_t)((BM * BK) >> 4);
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
-            umma_f8(tmem_base + acc.slot * NT, td + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), a.idesc, kk > 0 ? 1u : 0u);
+            umma_f8(tmem_base + acc.slot * C::kAccCols, td + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), a.idesc, kk > 0 ? 1u : 0u);
           umma_commit(&acc_full[acc.slot]);
           umma_commit(&empty[r.slot]);
         }
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
     const int part = (warp - 4) >> 2;  // columns kCols * part .. of the tile
     const int et = threadIdx.x - 128;
     const int r4 = lane >> 2, c4 = 2 * (lane & 3);  // this thread's rows r4 + 8 i and columns c4 + 8 j + {0, 1}
-    constexpr int J = C::kCols < 32 ? 2 : 4, NQ = C::kCols / (8 * J);  // 8-column groups per load, loads per block
+    constexpr int NQ = (C::kCols + 31) / 32;  // loads per block: 32 columns each, the last one what is left (16 or 32)
     constexpr int SR = C::kScaleRow;
     uint32_t group = 0;
     Ring<C::kAccs> at;  // the accumulator of the block in hand
@@ -368,11 +369,17 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
           // block of 128 x 128 1000 cycles instead of 700).
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            uint32_t v[2][4 * J];  // [16-row half]
+            const int groups = C::kCols - 32 * q >= 32 ? 4 : 2;  // of 8 columns
+            uint32_t v[2][16];  // [16-row half]
             if (rows_here) {
-              const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + at.slot * NT + part * C::kCols + 8 * J * q;
-              tmem_ld<J>(taddr, v[0]);
-              tmem_ld<J>(taddr + (16u << 16), v[1]);
+              const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + at.slot * C::kAccCols + part * C::kCols + 32 * q;
+              if (groups == 4) {
+                tmem_ld<4>(taddr, v[0]);
+                tmem_ld<4>(taddr + (16u << 16), v[1]);
+              } else {
+                tmem_ld<2>(taddr, v[0]);
+                tmem_ld<2>(taddr + (16u << 16), v[1]);
+              }
               tmem_wait();
             }
             if (q == NQ - 1) {  // the last columns are in registers: the accumulator goes back to the MMAs
@@ -383,14 +390,14 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
             }
             if (!rows_here) continue;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
+            for (int j = 0; j < groups; ++j) {
               uint64_t cs = 0;
-              if constexpr (!BLOCK) cs = *reinterpret_cast<const uint64_t*>(csc + 8 * (J * q + j));
+              if constexpr (!BLOCK) cs = *reinterpret_cast<const uint64_t*>(csc + 8 * (4 * q + j));
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint32_t* p = &v[i >> 1][4 * j + 2 * (i & 1)];
                 const uint64_t pp = pack2(p[0], p[1]);
-                acc[i][J * q + j] = fma2(BLOCK ? pp : mul2(pp, cs), rs[i], acc[i][J * q + j]);
+                acc[i][4 * q + j] = fma2(BLOCK ? pp : mul2(pp, cs), rs[i], acc[i][4 * q + j]);
               }
             }
           }
@@ -922,7 +929,8 @@ struct Plan {
 
 // Form, tile width and split of the blocks with the lowest estimated time in cycles, from times of single sizes: a
 // block takes a CTA of the single form 480 + 3.6 NT (the epilogue's way through TMEM; NT = 32, 64, 128:
-// 17 x 4096 x 4096 in 12.8, 15.7, 17.3 us) and a pair 1100 for four times the widest tile's area (1600 with a scale per weight row); a unit takes 2000 or
+// 17 x 4096 x 4096 in 12.8, 15.7, 17.3 us; 96 where 128 leaves CTAs idle and 64 fills them twice: 333 x 4099 x 11008
+// in 49.5 us without it, 44.5 with it) and a pair 1100 for four times the widest tile's area (1600 with a scale per weight row); a unit takes 2000 or
 // 6000 for its fill and its end; split sums are written and read back at about 3000 bytes per cycle of the
 // whole GPU, plus a launch.
 Plan make_plan(int64_t m, int64_t n, int64_t k, bool block) {
@@ -945,7 +953,9 @@ Plan make_plan(int64_t m, int64_t n, int64_t k, bool block) {
       }
     }
   };
-  for (int nt = 32; nt <= 128; nt *= 2) consider(nt, (m + BM - 1) / BM, (n + nt - 1) / nt, 1, 480.0 + 3.6 * nt, 2000.0);
+  for (int nt = 32; nt <= 128; nt += 32)
+    if (nt != 96 || !block)  // 128 weight rows that share a scale do not divide into 96
+      consider(nt, (m + BM - 1) / BM, (n + nt - 1) / nt, 1, 480.0 + 3.6 * nt, 2000.0);
   if (m > BM) consider(PN, (m + 2 * BM - 1) / (2 * BM), (n + PN - 1) / PN, 2, block ? 1100.0 : 1600.0, 6000.0);
   return best;
 }
@@ -1026,6 +1036,7 @@ gptq_status launch_typed(const Plan& p, bool block, const CUtensorMap& t, const 
   switch (p.nt) {
     case 32: st = launch_block<32, TY>(block, t, w, a, sms, s); break;
     case 64: st = launch_block<64, TY>(block, t, w, a, sms, s); break;
+    case 96: st = launch<96, false, TY>(t, w, a, sms, s); break;  // never with block scales
     case 128: st = launch_block<128, TY>(block, t, w, a, sms, s); break;
     default: {
       if (a.partial == nullptr) {

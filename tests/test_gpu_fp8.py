@@ -156,6 +156,14 @@ def test_matmul_against_fp64(m, n, k, dtype, rows):
     _check_matmul(_matmul(A, sa, B, sb, rows, dtype), A, sa, B, sb, rows)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(140, 4800, 256), (257, 4000, 512), (60, 11259, 1120), (170, 3508, 5776), (37, 1545, 6736)])
+def test_matmul_in_tiles_of_96_weight_rows(m, n, k, dtype):
+    """Sizes at which 96 weight rows a tile fill the GPU best, whole and with the blocks split; odd row counts."""
+    A, sa, B, sb = _operands(m, n, k, 1, m + n, S.dev())
+    _check_matmul(_matmul(A, sa, B, sb, 1, dtype), A, sa, B, sb, 1)
+
+
 def test_matmul_is_deterministic_and_keeps_to_its_rows():
     """Two calls give equal bits; Y's memory behind the last row, and the operands, stay as they were."""
     m, n, k = 19, 1000, 4096
