@@ -786,13 +786,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
 }
 
 // ------------------------------------------------------------------------------------------------
-// A few tokens (up to 8).  The weights' bytes are all that counts, and a tile's way through tensor maps, TMEM and a
-// second launch for split sums takes longer than reading them (1 x 4096 x 4096: 9.9 us, here 6.6, 2.5 TB/s with the
-// launch in it; 1 x 12288 x 16384: 47 us, 4.3 TB/s).  Here a CTA takes 16
-// weight rows, its 8 warps the blocks in turn; codes go straight from global memory into registers, two
-// blocks ahead, become fp16 pairs (exact) and fragments of mma.m16n8k16 with the weights on the M
-// side; the warps' scaled sums meet in shared memory, added in order.
-constexpr int kFewTokens = 8;
+// A few tokens (up to 8, or 16 with smaller weights).  The weights' bytes are all that counts, and a tile's way through
+// tensor maps, TMEM and a second launch for split sums takes longer than reading them (1 x 4096 x 4096: 9.9 us, here
+// 6.5, 2.6 TB/s with the launch in it; 1 x 12288 x 16384: 47 us, 4.3 TB/s).  Here a CTA takes 16 weight rows, its 8
+// warps the blocks in turn; codes go straight from global memory into registers, two blocks ahead, become fp16 pairs
+// (exact) and fragments of mma.m16n8k16 with the weights on the M side; the warps' scaled sums meet in shared
+// memory, added in order.
+// Every warp converts all tokens for itself, so with 9 to 16 of them large weights are better off in tiles: 16 x 768 x
+// 768 2.6 us here, 4.8 in tiles, 4096 x 4096 8.4 and 10.8, 11008 x 4096 19.9 and 17.2, 12288 x 12288 52 and 39 (up to
+// 8 tokens: 39 and 38).  With 32 the tiles win from 4096 x 4096 on (12.4 and 11.4).
+bool few_tokens(int64_t m, int64_t n, int64_t k) { return m <= 8 || (m <= 16 && n * k <= 1 << 25); }
 constexpr int kFewWarps = 8;
 constexpr int kFewBlocks = 2;  // blocks a warp works on while as many are on their way
 
@@ -809,15 +812,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A lane holds columns 16 t .. 16 t + 15 of each half of a block, of weight rows g and g + 8 and of token g; which
-// columns meet in one MMA is free as long as both operands agree.
-template <bool BLOCK, typename TY>
+// A lane holds columns 16 t .. 16 t + 15 of each half of a block, of weight rows g and g + 8 and of tokens g, g + 8, ..
+// (NG of them); which columns meet in one MMA is free as long as both operands agree.
+template <int NG, bool BLOCK, typename TY>
 __global__ void __launch_bounds__(kFewWarps * 32, 2) fp8_matmul_few_kernel(const uint8_t* __restrict__ A,
                                                                            const float* __restrict__ a_scales,
                                                                            const uint8_t* __restrict__ B,
                                                                            const float* __restrict__ b_scales, int m,
                                                                            int n, int k, int kb, TY* __restrict__ Y) {
-  __shared__ float sums[kFewWarps][16][kFewTokens + 1];
+  __shared__ float sums[kFewWarps][16][8 * NG + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int row0 = blockIdx.x * 16;
@@ -826,11 +829,16 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) fp8_matmul_few_kernel(const
   const uint8_t* w1 = B + (int64_t)r1 * k + 16 * t;
   const float* s0 = b_scales + (int64_t)(BLOCK ? r0 >> 7 : r0) * kb;
   const float* s1 = b_scales + (int64_t)(BLOCK ? r1 >> 7 : r1) * kb;
-  const uint8_t* x = A + (int64_t)g * k + 16 * t;
-  const bool token_here = g < m;
-  const float* e0 = a_scales + (int64_t)min(2 * t, m - 1) * kb;
-  const float* e1 = a_scales + (int64_t)min(2 * t + 1, m - 1) * kb;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint8_t* x[NG];
+  const float *e0[NG], *e1[NG];
+  float acc[NG][4];
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    x[n] = A + (int64_t)min(8 * n + g, m - 1) * k + 16 * t;  // past the last token: it once more, nobody reads the sums
+    e0[n] = a_scales + (int64_t)min(8 * n + 2 * t, m - 1) * kb;
+    e1[n] = a_scales + (int64_t)min(8 * n + 2 * t + 1, m - 1) * kb;
+    acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+  }
   const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4 next[kFewBlocks][4];
   auto load = [&](int b0) {
@@ -857,12 +865,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) fp8_matmul_few_kernel(const
     for (int i = 0; i < kFewBlocks; ++i) {
       const int b = b0 + i * kFewWarps;
       if (b >= kb) break;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float sum[NG][4];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.0f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool ok = token_here && b * BK + 64 * h + 16 * t < k;
-        const uint4 xv = ok ? __ldg(reinterpret_cast<const uint4*>(x + b * BK + 64 * h)) : zero;
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+        const bool ok = b * BK + 64 * h + 16 * t < k;
+        uint4 xv[NG];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) xv[n] = ok ? __ldg(reinterpret_cast<const uint4*>(x[n] + b * BK + 64 * h)) : zero;
         const uint4 u0 = w[i][2 * h], u1 = w[i][2 * h + 1];
         const uint32_t a0[4] = {u0.x, u0.y, u0.z, u0.w}, a1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
@@ -870,22 +881,33 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) fp8_matmul_few_kernel(const
           uint32_t p0, p1, p2, p3, y0, y1;
           e4m3_to_f16(a0[q], p0, p2);
           e4m3_to_f16(a1[q], p1, p3);
-          e4m3_to_f16(xw[q], y0, y1);
-          mma_f16(sum, p0, p1, p2, p3, y0, y1);
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            const uint32_t xw[4] = {xv[n].x, xv[n].y, xv[n].z, xv[n].w};
+            e4m3_to_f16(xw[q], y0, y1);
+            mma_f16(sum[n], p0, p1, p2, p3, y0, y1);
+          }
         }
       }
-      const float f0 = __ldg(s0 + b), f1 = __ldg(s1 + b), c0 = __ldg(e0 + b), c1 = __ldg(e1 + b);
-      acc[0] = fmaf(sum[0] * c0, f0, acc[0]);
-      acc[1] = fmaf(sum[1] * c1, f0, acc[1]);
-      acc[2] = fmaf(sum[2] * c0, f1, acc[2]);
-      acc[3] = fmaf(sum[3] * c1, f1, acc[3]);
+      const float f0 = __ldg(s0 + b), f1 = __ldg(s1 + b);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const float c0 = __ldg(e0[n] + b), c1 = __ldg(e1[n] + b);
+        acc[n][0] = fmaf(sum[n][0] * c0, f0, acc[n][0]);
+        acc[n][1] = fmaf(sum[n][1] * c1, f0, acc[n][1]);
+        acc[n][2] = fmaf(sum[n][2] * c0, f1, acc[n][2]);
+        acc[n][3] = fmaf(sum[n][3] * c1, f1, acc[n][3]);
+      }
     }
   }
-  sums[warp][g][2 * t] = acc[0], sums[warp][g][2 * t + 1] = acc[1];
-  sums[warp][g + 8][2 * t] = acc[2], sums[warp][g + 8][2 * t + 1] = acc[3];
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    sums[warp][g][8 * n + 2 * t] = acc[n][0], sums[warp][g][8 * n + 2 * t + 1] = acc[n][1];
+    sums[warp][g + 8][8 * n + 2 * t] = acc[n][2], sums[warp][g + 8][8 * n + 2 * t + 1] = acc[n][3];
+  }
   __syncthreads();
-  if (threadIdx.x < 16 * m) {  // at most 128
-    const int r = threadIdx.x & 15, tok = threadIdx.x >> 4;
+  for (int i = threadIdx.x; i < 16 * m; i += kFewWarps * 32) {
+    const int r = i & 15, tok = i >> 4;
     if (row0 + r < n) {
       float s = 0.0f;
 #pragma unroll
@@ -901,10 +923,9 @@ gptq_status launch_few(const void* A, const float* a_scales, const void* B, cons
   const uint8_t *a = static_cast<const uint8_t*>(A), *b = static_cast<const uint8_t*>(B);
   const unsigned grid = (unsigned)((n + 15) / 16);
   const int kb = (k + BK - 1) / BK;
-  if (block)
-    fp8_matmul_few_kernel<true, TY><<<grid, kFewWarps * 32, 0, s>>>(a, a_scales, b, b_scales, m, n, k, kb, Y);
-  else
-    fp8_matmul_few_kernel<false, TY><<<grid, kFewWarps * 32, 0, s>>>(a, a_scales, b, b_scales, m, n, k, kb, Y);
+  auto kernel = m <= 8 ? (block ? fp8_matmul_few_kernel<1, true, TY> : fp8_matmul_few_kernel<1, false, TY>)
+                       : (block ? fp8_matmul_few_kernel<2, true, TY> : fp8_matmul_few_kernel<2, false, TY>);
+  kernel<<<grid, kFewWarps * 32, 0, s>>>(a, a_scales, b, b_scales, m, n, k, kb, Y);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -1059,7 +1080,7 @@ gptq_status launch_typed(const Plan& p, bool block, const CUtensorMap& t, const 
 
 
 size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k) {
-  if (m <= kFewTokens) return 0;
+  if (few_tokens(m, n, k)) return 0;
   size_t need = 0;  // for either kind of weight scales
   for (int block = 0; block < 2; ++block) {
     const Plan p = make_plan(m, n, k, block != 0);
@@ -1071,7 +1092,7 @@ size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k) {
 gptq_status fp8_matmul_launch(const void* A, const float* a_scales, const void* B, const float* b_scales,
                               int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* Y, int32_t y_dtype,
                               int32_t* status, void* workspace, cudaStream_t stream) {
-  if (m <= kFewTokens) {
+  if (few_tokens(m, n, k)) {
     const bool block = b_block_rows == 128;
     switch (y_dtype) {
       case GPTQ_BF16: return launch_few(A, a_scales, B, b_scales, block, (int)m, (int)n, (int)k, static_cast<__nv_bfloat16*>(Y), stream);

@@ -156,6 +156,14 @@ def test_matmul_against_fp64(m, n, k, dtype, rows):
     _check_matmul(_matmul(A, sa, B, sb, rows, dtype), A, sa, B, sb, rows)
 
 
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("m,n,k", [(9, 33, 272), (15, 200, 144), (16, 129, 2064), (16, 4096, 8192), (16, 4112, 8192), (17, 48, 256)])
+def test_matmul_of_up_to_16_tokens(m, n, k, rows):
+    """The second group of eight tokens, and both sides of the weights' size that ends it."""
+    A, sa, B, sb = _operands(m, n, k, rows, m + n, S.dev())
+    _check_matmul(_matmul(A, sa, B, sb, rows, torch.float32), A, sa, B, sb, rows)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("m,n,k", [(140, 4800, 256), (257, 4000, 512), (60, 11259, 1120), (170, 3508, 5776), (37, 1545, 6736)])
 def test_matmul_in_tiles_of_96_weight_rows(m, n, k, dtype):
