@@ -377,11 +377,13 @@ __device__ __forceinline__ void route(const float* logits, const Route& a) {
   if (logits != nullptr) {
     for (int t = warp; t < tokens; t += WARPS) {
       constexpr int N = kMaxExperts / 32;
+      const int n = (experts + 31) >> 5;  // of them in use
       float l[N];
       uint32_t key[N];
       float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
+        if (i >= n) break;
         const int e = lane + 32 * i;
         l[i] = e < experts ? __ldcg(logits + t * experts + e) : -INFINITY;
         key[i] = e < experts ? max(ordered(l[i]), 1u) : 0u;  // 0: not there, or chosen before
@@ -390,25 +392,33 @@ __device__ __forceinline__ void route(const float* logits, const Route& a) {
       mx = warp_max(mx);
       float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i) {
+        if (i >= n) break;
         if (lane + 32 * i < experts) sum += expf(l[i] - mx);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       float mine = 0.0f, chosen = 0.0f;  // lane k keeps the k-th weight
       for (int k = 0; k < top_k; ++k) {
-        uint32_t best = 0;
+        uint32_t best = 0, at = 0xffffffffu;
 #pragma unroll
-        for (int i = 0; i < N; ++i) best = max(best, key[i]);
+        for (int i = 0; i < N; ++i) {
+          if (i >= n) break;
+          best = max(best, key[i]);
+        }
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        uint32_t at = 0xffffffffu;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+          if (i >= n) break;
           if (key[i] == top) at = min(at, (uint32_t)(lane + 32 * i));
+        }
         const int e = (int)__reduce_min_sync(0xffffffffu, at);
         float le = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+          if (i >= n) break;
           if (lane + 32 * i == e) le = l[i], key[i] = 0;
+        }
         le = __shfl_sync(0xffffffffu, le, e & 31);
         const float w = expf(le - mx) / sum;
         chosen += w;
