@@ -178,6 +178,29 @@ def test_given_routing_with_repeats_and_bad_ids():
     assert (c.Y[3] == 0).all()
 
 
+@pytest.mark.parametrize("t,e,top", [(8, 8, 8), (8, 9, 2), (9, 8, 2), (3, 32, 16), (3, 33, 16), (2, 64, 16), (5, 65, 3), (1, 255, 16)])
+def test_choice_over_any_number_of_experts(t, e, top):
+    """Around the counts at which the logits get a launch of their own, and around the 32 experts that a warp holds at a
+    time; as many choices as experts."""
+    c = Case(t, e, top, 64, 32, 4, 0, hf, ff, RELU)
+    c.run(g.GPTQ_MOE_RENORMALIZE)
+    assert g.gptq_read_status(c.st)[0] == g.GPTQ_OK
+    c.check_routing(1)
+    c.check()
+
+
+@pytest.mark.parametrize("t,e,top", [(64, 20, 5), (64, 256, 16), (40, 2, 16)])
+def test_given_routing_of_many_tokens(t, e, top):
+    """The caller's routing with repeats, more pairs than a warp looks at in one step; one expert is never named."""
+    c = Case(t, e, top, 96, 64, 3, 32, bf, ff, RELU)
+    gen = torch.Generator().manual_seed(t + e)
+    c.w.copy_(torch.rand(t, top, generator=gen))
+    c.ids.copy_(torch.randint(0, e - 1, (t, top), generator=gen).to(torch.int32))
+    c.run(router=False)
+    assert g.gptq_read_status(c.st)[0] == g.GPTQ_OK
+    c.check()
+
+
 def test_deterministic_and_inputs_untouched():
     c = Case(40, 8, 3, 512, 256, 4, 128, hf, ff, SILU)
     before = [t.clone() for t in (c.x, c.router, *c.up, *c.gate, *c.down)]
