@@ -344,7 +344,7 @@ GPTQ_API size_t gptq_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  *                as gptq_quantize_layer writes them.  gate: all NULL with GPTQ_ACT_RELU.
  *   down         n_experts matrices [d, f] likewise.
  *   topk_ids     int32 [tokens, top_k], topk_weights fp32 [tokens, top_k]: outputs with a router, inputs
- *                without.  As inputs the same expert may be given twice; an id outside [0, n_experts) is recorded
+ *                without (taken as they are, whatever the flags).  As inputs the same expert may be given twice; an id outside [0, n_experts) is recorded
  *                as {GPTQ_ERR_ARG, its place} in dev_status and adds nothing.
  *   Y            [tokens, d] in y_dtype, rounded once from the fp32 sum.
  *   dev_status   int32[2], zeroed by the caller once, not cleared by the call.

@@ -951,9 +951,9 @@ struct Plan {
 // Form, tile width and split of the blocks with the lowest estimated time in cycles, from times of single sizes: a
 // block takes a CTA of the single form 480 + 3.6 NT (the epilogue's way through TMEM; NT = 32, 64, 128:
 // 17 x 4096 x 4096 in 12.8, 15.7, 17.3 us; 96 where 128 leaves CTAs idle and 64 fills them twice: 333 x 4099 x 11008
-// in 49.5 us without it, 44.5 with it) and a pair 1100 for four times the widest tile's area (1600 with a scale per weight row); a unit takes 2000 or
-// 6000 for its fill and its end; split sums are written and read back at about 3000 bytes per cycle of the
-// whole GPU, plus a launch.
+// in 49.5 us without it, 44.5 with it) and a pair 1100 for four times the widest tile's area (1600 with a scale per
+// weight row); a unit takes 2000 or 6000 for its fill and its end; split sums are written and read back at about
+// 3000 bytes per cycle of the whole GPU, plus a launch.
 Plan make_plan(int64_t m, int64_t n, int64_t k, bool block) {
   Plan best = {};
   double best_cost = 1e300;

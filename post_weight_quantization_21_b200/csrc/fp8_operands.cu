@@ -241,8 +241,8 @@ __device__ __forceinline__ uint32_t nibbles(const uint32_t (&w)[BITS], int k) {
 // A thread turns one unit of 32 codes (BITS words) into 32 e4m3 integers q - zero: the bytes for q = 0 .. 2^b - 1 come
 // from a table by zero point, and a byte permutation with the codes as selectors picks four at a time (two
 // and a blend at 4 bits, where the top bit chooses the half of the table).  One instruction or two a code; masking,
-// one FMA and a conversion per code took 17.5 us for 11008 x 4096 codes of 4 bits, this 14.7 (4.6 TB/s).  Zero points outside the
-// grid take that way.
+// one FMA and a conversion per code took 17.5 us for 11008 x 4096 codes of 4 bits, this 14.9 (4.6 TB/s).  Zero
+// points outside the grid take that way.
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) fp8_from_packed_kernel(const uint32_t* __restrict__ packed,
                                                                    const float* __restrict__ scales,
